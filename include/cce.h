@@ -507,6 +507,78 @@ cce_status cce_forward_noalloc(const void* H, int64_t M, const cce_head* W,
                                float* tgt_logit, float* blockmax,
                                uint32_t* status, cce_stream_t stream);
 
+/* ==========================================================================
+ * Operators around the head: 8-bit rows and weights, the final norm with an
+ * 8-bit checkpoint of its input.
+ *
+ * The conventions at the top of this file hold, with these additions:
+ * - Matrices are row-major; ldX is the distance of two rows, in elements
+ *   (bytes for 8-bit codes), at least the number of columns.  Elements behind
+ *   the last column of a row are neither read nor written.  Any alignment of
+ *   the element type is taken; rows on 16-byte boundaries (8 for codes) are
+ *   the fast ones.
+ * - Outputs overlap no input and no other output.
+ * - A workspace serves one call at a time: calls that may overlap on the GPU,
+ *   captured graphs that may replay at the same time included, need one each.
+ *
+ * 8-bit format ("e4m3 groups of 128").  A group holds e4m3 codes q and one
+ * fp32 scale s; the values are q * s.  With m = max(2^-90, max |x| over the
+ * group),
+ *   s = m / 448,   q = e4m3(x * (448 * (1 / m))),
+ * quotients and products rounded in fp32, codes to nearest even.  A
+ * group is 128 consecutive columns of a row (activations, checkpoints; scales
+ * [M, ceil(D/128)], dense) or a 128 x 128 block (weights; scales
+ * [ceil(N/128), ceil(K/128)], dense); the last ones may be smaller.  A NaN
+ * stays one; a group that holds an infinity restores as NaN.
+ * ======================================================================== */
+
+/* Codes and scales of the rows of X [M, D], f32 or bf16, D <= 65,536. */
+cce_status cce_fp8_quant_rows(const void* X, cce_dtype x_dtype, int64_t M,
+                              int64_t D, int64_t ldx, uint8_t* Q, int64_t ldq,
+                              float* S, cce_stream_t stream);
+/* Codes and scales of the 128 x 128 blocks of W [N, K], f32 or bf16,
+ * K <= 65,536, N <= 65,535 * 128. */
+cce_status cce_fp8_quant_blocks(const void* W, cce_dtype w_dtype, int64_t N,
+                                int64_t K, int64_t ldw, uint8_t* Q,
+                                int64_t ldq, float* S, cce_stream_t stream);
+
+/*
+ * Final norm, the step that makes the head's rows from the residual stream:
+ *   rstd[m] = 1 / sqrt(mean_d X[m,d]^2 + eps),  H[m,d] = X[m,d] rstd[m] w[d]
+ * X: [M, D], f32 or bf16, D <= 16,384; w: [D], f32 or bf16.  Computed in fp32.
+ * Outputs, each optional, at least one:
+ *   H: [M, D], f32 or bf16 (the H of cce_forward);
+ *   H8, Hs: the rows of H in 8 bits, made from the fp32 values (the A of
+ *     cce_fp8_matmul);
+ *   X8, Xs, rstd: what cce_norm_backward needs, an 8-bit checkpoint of X that
+ *     takes the place of X between the passes (1.03 bytes an element).
+ * One kernel; X is read once.
+ */
+cce_status cce_norm_forward(const void* X, cce_dtype x_dtype, int64_t M,
+                            int64_t D, int64_t ldx, const void* w,
+                            cce_dtype w_dtype, double eps, void* H,
+                            cce_dtype h_dtype, int64_t ldh, uint8_t* H8,
+                            int64_t ldh8, float* Hs, uint8_t* X8, int64_t ldx8,
+                            float* Xs, float* rstd, cce_stream_t stream);
+
+/*
+ * Gradient of the final norm from its checkpoint.  With n = X8 Xs rstd (the
+ * normalised row as the checkpoint holds it) and g = dH w:
+ *   dX = rstd (g - n mean_d(g n)),   dW[d] = sum_m dH[m,d] n[m,d]
+ * dH: [M, D], f32 or bf16 (the dH of cce_backward_dh).  dX: [M, D], f32 or
+ * bf16, overwritten.  dW: fp32 [D], overwritten, or NULL (a frozen norm; ws
+ * may then be NULL).  rstd is taken as given (the forward's, from the exact
+ * X).  Sums in fp32, in an order that depends on the sizes alone.
+ * ws: cce_norm_backward_workspace_bytes(M, D) bytes (0: invalid sizes).
+ */
+size_t cce_norm_backward_workspace_bytes(int64_t M, int64_t D);
+cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs,
+                             const float* rstd, int64_t M, int64_t D,
+                             const void* w, cce_dtype w_dtype, const void* dH,
+                             cce_dtype dh_dtype, int64_t lddh, void* dX,
+                             cce_dtype dx_dtype, int64_t lddx, float* dW,
+                             void* ws, size_t ws_bytes, cce_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -130,6 +130,26 @@ _SIGS = {
     "cce_prefix_scatter": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                           ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                           ctypes.c_void_p]),
+    "cce_fp8_quant_rows": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                          ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                          ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "cce_fp8_quant_blocks": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                            ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "cce_norm_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                        ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_int, ctypes.c_double, ctypes.c_void_p,
+                                        ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p]),
+    "cce_norm_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
+    "cce_norm_backward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
+                                         ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                         ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                         ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "cce_profile_enable": (None, [ctypes.c_int]),
     "cce_profile_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_double),
                                         ctypes.POINTER(ctypes.c_longlong), ctypes.c_int]),
@@ -525,3 +545,147 @@ def cce_query_plan(M: int, H_dtype: int, head: "Head | _Head", ws_bytes: int) ->
     _check(lib().cce_query_plan(M, H_dtype, ctypes.byref(h), ws_bytes, ctypes.byref(out)),
            "cce_query_plan")
     return {n: getattr(out, n) for n, _ in _Plan._fields_}
+
+
+# ----------------------------------------------------------------------------
+# operators around the head
+# ----------------------------------------------------------------------------
+#
+# Tensors: matrices may have any row stride (the columns are contiguous);
+# 8-bit codes are torch.float8_e4m3fn; scales and per-row vectors are dense
+# fp32.  A shape, type or stride the library would misread raises ValueError
+# before the call; everything else is left to the library's own checks.  The
+# call is made on the tensors' device and, without ``stream``, on that device's
+# current stream.
+
+QGROUP = 128
+
+
+def fp8_groups(n: int) -> int:
+    """Number of groups of 128 that ``n`` columns (or rows) fall into."""
+    return -(-int(n) // QGROUP)
+
+
+def fp8_empty(rows: int, cols: int, device="cuda"):
+    """Room for 8-bit codes [rows, cols] with rows on 16-byte boundaries, as
+    cce_fp8_matmul wants them."""
+    return torch.empty(rows, -(-cols // 16) * 16, dtype=torch.float8_e4m3fn,
+                       device=device)[:, :cols]
+
+
+_MAT_TYPES = {torch.float32: CCE_F32, torch.bfloat16: CCE_BF16}
+_CODES = {torch.float8_e4m3fn: 0}
+_F32 = {torch.float32: CCE_F32}
+
+
+def _bad(name, t, types, shape, dev):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the others on cuda:{dev}")
+    if t.dtype not in types:
+        raise ValueError(f"{name}: {t.dtype} not supported")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    raise ValueError(f"{name}: strides {t.stride()} not supported")
+
+
+def _mat(name, t, types, rows, cols, dev):
+    """Address, type code and row stride of a matrix with contiguous rows."""
+    if t.get_device() != dev or dev < 0 or t.dtype not in types or t.shape != (rows, cols):
+        _bad(name, t, types, (rows, cols), dev)
+    s0, s1 = t.stride()
+    if (s1 != 1 and cols > 1) or (s0 < cols and rows > 1):
+        _bad(name, t, types, (rows, cols), dev)
+    return t.data_ptr(), types[t.dtype], (s0 if rows > 1 else cols)
+
+
+def _dense(name, t, types, shape, dev):
+    """Address of a contiguous tensor of this shape."""
+    if (t.get_device() != dev or dev < 0 or t.dtype not in types or t.shape != shape
+            or not t.is_contiguous()):
+        _bad(name, t, types, shape, dev)
+    return t.data_ptr()
+
+
+def _workspace(ws, dev):
+    if ws.get_device() != dev or dev < 0 or not ws.is_contiguous() or ws.dtype is not torch.uint8:
+        _bad("ws", ws, {torch.uint8: 0}, tuple(ws.shape), dev)
+    return ws.data_ptr(), ws.numel()
+
+
+def _run(name, dev, stream, *args):
+    """The library's call with the tensors' device current."""
+    cur = torch._C._cuda_getDevice()
+    if cur != dev:
+        torch.cuda.set_device(dev)
+    try:
+        s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        st = getattr(lib(), name)(*args, s)
+    finally:
+        if cur != dev:
+            torch.cuda.set_device(cur)
+    if st != 0:
+        raise CCEError(st, name)
+
+
+def cce_fp8_quant_rows(X, Q, S, stream=None):
+    """8-bit codes Q [M, D] and scales S [M, ceil(D/128)] of the rows of X
+    (f32 or bf16), one scale for each 128 columns."""
+    (M, D), dev = X.shape, X.get_device()
+    x, xt, ldx = _mat("X", X, _MAT_TYPES, M, D, dev)
+    q, _, ldq = _mat("Q", Q, _CODES, M, D, dev)
+    _run("cce_fp8_quant_rows", dev, stream, x, xt, M, D, ldx, q, ldq,
+         _dense("S", S, _F32, (M, fp8_groups(D)), dev))
+
+
+def cce_fp8_quant_blocks(W, Q, S, stream=None):
+    """8-bit codes Q [N, K] and scales S [ceil(N/128), ceil(K/128)] of the
+    128 x 128 blocks of W (f32 or bf16)."""
+    (N, K), dev = W.shape, W.get_device()
+    x, xt, ldx = _mat("W", W, _MAT_TYPES, N, K, dev)
+    q, _, ldq = _mat("Q", Q, _CODES, N, K, dev)
+    _run("cce_fp8_quant_blocks", dev, stream, x, xt, N, K, ldx, q, ldq,
+         _dense("S", S, _F32, (fp8_groups(N), fp8_groups(K)), dev))
+
+
+def _codes_of(name, q, s, M, D, dev):
+    if q is None and s is None:
+        return None, 0, None
+    if q is None or s is None:
+        raise ValueError(f"{name}: codes and scales go together")
+    p, _, ld = _mat(name, q, _CODES, M, D, dev)
+    return p, ld, _dense(name + " scales", s, _F32, (M, fp8_groups(D)), dev)
+
+
+def cce_norm_forward(X, w, eps, H=None, H8=None, Hs=None, X8=None, Xs=None, rstd=None,
+                     stream=None):
+    """Final norm H = X / sqrt(mean(X^2) + eps) * w, row by row, with its
+    optional outputs: H (f32 or bf16), its 8-bit form (H8, Hs) and the
+    checkpoint (X8, Xs, rstd) that cce_norm_backward reads."""
+    (M, D), dev = X.shape, X.get_device()
+    x, xt, ldx = _mat("X", X, _MAT_TYPES, M, D, dev)
+    h, ht, ldh = (None, CCE_BF16, 0) if H is None else _mat("H", H, _MAT_TYPES, M, D, dev)
+    h8, ldh8, hs = _codes_of("H8", H8, Hs, M, D, dev)
+    x8, ldx8, xs = _codes_of("X8", X8, Xs, M, D, dev)
+    _run("cce_norm_forward", dev, stream, x, xt, M, D, ldx,
+         _dense("w", w, _MAT_TYPES, (D,), dev), _MAT_TYPES[w.dtype], eps, h, ht, ldh, h8, ldh8, hs,
+         x8, ldx8, xs, None if rstd is None else _dense("rstd", rstd, _F32, (M,), dev))
+
+
+def cce_norm_backward_workspace_bytes(M: int, D: int) -> int:
+    return int(lib().cce_norm_backward_workspace_bytes(M, D))
+
+
+def cce_norm_backward(X8, Xs, rstd, w, dH, dX, dW=None, ws=None, stream=None):
+    """Gradient of the final norm from its checkpoint: dX [M, D] (f32 or bf16)
+    and, unless the norm is frozen, dW fp32 [D]; ``ws``: uint8, at least
+    cce_norm_backward_workspace_bytes(M, D) long, needed for dW only."""
+    (M, D), dev = dH.shape, dH.get_device()
+    dh, dht, lddh = _mat("dH", dH, _MAT_TYPES, M, D, dev)
+    dx, dxt, lddx = _mat("dX", dX, _MAT_TYPES, M, D, dev)
+    x8, ldx8, xs = _codes_of("X8", X8, Xs, M, D, dev)
+    p, n = (None, 0) if ws is None else _workspace(ws, dev)
+    _run("cce_norm_backward", dev, stream, x8, ldx8, xs, _dense("rstd", rstd, _F32, (M,), dev),
+         M, D, _dense("w", w, _MAT_TYPES, (D,), dev), _MAT_TYPES[w.dtype], dh, dht, lddh, dx, dxt,
+         lddx, None if dW is None else _dense("dW", dW, _F32, (D,), dev), p, n)

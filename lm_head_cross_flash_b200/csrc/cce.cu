@@ -98,7 +98,8 @@ bool make_map(CUtensorMap* m, const void* ptr, bool bf16, uint64_t cols,
 // bracketed by a CUDA event pair recorded on its own stream.
 enum ProfKind {
   PK_SPLIT = 0, PK_LSE, PK_MERGE, PK_ORPO, PK_SKIP, PK_GRAD, PK_DH, PK_SELFTEST, PK_DHSUM,
-  PK_PREFIX, PK_DW, PK_DEQ, PK_FUSED, PK_FSUM, PK_SLICE, PK_SSUM, PK_QFWD, PK_N
+  PK_PREFIX, PK_DW, PK_DEQ, PK_FUSED, PK_FSUM, PK_SLICE, PK_SSUM, PK_QFWD,
+  PK_QUANT, PK_NORM, PK_N
 };
 const char* const kProfNames[PK_N] = {"operand_prep",  "fwd_lse_gemm", "lse_merge",
                                       "orpo_epilogue", "skip_plan",    "bwd_grad_gemm",
@@ -106,7 +107,8 @@ const char* const kProfNames[PK_N] = {"operand_prep",  "fwd_lse_gemm", "lse_merg
                                       "prefix_gather_scatter", "bwd_dw_gemm",
                                       "dequant_chunk", "bwd_fused",
                                       "fused_part_sum", "bwd_sliced",
-                                      "sliced_part_sum", "fwd_q_small_m"};
+                                      "sliced_part_sum", "fwd_q_small_m",
+                                      "fp8_quant", "final_norm"};
 struct ProfRec {
   int kind;
   cudaEvent_t a, b;
@@ -1977,3 +1979,5 @@ extern "C" cce_status cce_forward_noalloc(const void* H, int64_t M, const cce_he
       part_m, part_s, int(cols), int(M), labels, int(V), tgt, logp, lse, st_word);
   return launch_ok();
 }
+
+#include "head_ops.cuh"

@@ -1,0 +1,245 @@
+// head_ops.cuh — host side of the operators around the head (the last part of
+// include/cce.h): argument checks and launches.  Included once, by cce.cu,
+// behind the helpers it shares with the head's own entry points.
+#pragma once
+
+#include "row_ops.cuh"
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kMaxQuantD = int64_t(1) << 16;
+// A row lives in the registers of at most 512 threads, 4 pieces of 8 each.
+constexpr int64_t kMaxNormD = 512 * 4 * 8;
+
+bool dtype_ok(cce_dtype t) { return t == CCE_F32 || t == CCE_BF16; }
+int64_t dtype_bytes(cce_dtype t) { return t == CCE_F32 ? 4 : 2; }
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// Rows of `ld` elements of `bytes` each that all start on a 16-byte boundary.
+bool rows16(const void* p, int64_t ld, int64_t bytes) {
+  return aligned_to(p, 16) && ld * bytes % 16 == 0;
+}
+
+cce_status check_matrix(const void* p, cce_dtype t, int64_t rows, int64_t cols, int64_t ld) {
+  if (p == nullptr || !dtype_ok(t) || rows <= 0 || cols <= 0 || ld < cols)
+    return CCE_ERR_INVALID_ARGUMENT;
+  if (!aligned_to(p, uintptr_t(dtype_bytes(t)))) return CCE_ERR_INVALID_ARGUMENT;
+  if (rows > kMaxRows || cols > kMaxRows || ld > (int64_t(1) << 32)) return CCE_ERR_UNSUPPORTED;
+  return CCE_OK;
+}
+
+cce_status check_codes(const void* q, int64_t ldq, const float* s, int64_t cols) {
+  if (q == nullptr || s == nullptr || ldq < cols || !aligned_to(s, 4))
+    return CCE_ERR_INVALID_ARGUMENT;
+  return ldq > (int64_t(1) << 32) ? CCE_ERR_UNSUPPORTED : CCE_OK;
+}
+
+bool codes8(const void* q, int64_t ldq) { return aligned_to(q, 8) && ldq % 8 == 0; }
+QMat qmat(const void* q, int64_t ldq, const float* s, int64_t cols) {
+  QMat m;
+  m.q = static_cast<uint8_t*>(const_cast<void*>(q));
+  m.ldq = ldq;
+  m.s = const_cast<float*>(s);
+  m.lds = ceil_div(cols, QGROUP);
+  return m;
+}
+
+// Calls f with the types and the team shape (threads per row, pieces per
+// thread) of a row of D elements.
+template <typename T>
+struct Tag { using type = T; };
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+template <typename F>
+void with_type(cce_dtype t, F f) {
+  if (t == CCE_F32) f(Tag<float>());
+  else f(Tag<__nv_bfloat16>());
+}
+template <typename F>
+void with_bool(bool b, F f) {
+  if (b) f(std::true_type());
+  else f(std::false_type());
+}
+// Unaligned rows (vec false) take one of three shapes only.
+template <bool VEC, typename F>
+void with_team(int64_t D, F f) {
+  const int64_t n8 = ceil_div(D, 8);
+  if (n8 <= 32) return f(Int<32>(), Int<1>());
+  if constexpr (VEC) {
+    if (n8 <= 64) return f(Int<64>(), Int<1>());
+    if (n8 <= 128) return f(Int<128>(), Int<1>());
+  }
+  if (n8 <= 256) return f(Int<256>(), Int<1>());
+  if constexpr (VEC) {
+    if (n8 <= 512) return f(Int<512>(), Int<1>());
+    if (n8 <= 1024) return f(Int<512>(), Int<2>());
+  }
+  f(Int<512>(), Int<4>());
+}
+
+// Blocks of the norm's backward: enough to fill the SMs, each with several
+// rows where there are many, so that the parts of dw stay a small share.
+int norm_bwd_blocks(int64_t M, int64_t D) {
+  int rpb = 1;
+  with_team<true>(D, [&](auto tpr, auto) { rpb = norm_block(tpr()) / tpr(); });
+  const int64_t per_sm = D > 256 * 8 ? 2 : 4;
+  return int(std::max<int64_t>(1, std::min<int64_t>(ceil_div(M, rpb), per_sm * sm_count_guess())));
+}
+
+}  // namespace
+
+extern "C" {
+
+cce_status cce_fp8_quant_rows(const void* X, cce_dtype x_dtype, int64_t M, int64_t D, int64_t ldx,
+                              uint8_t* Q, int64_t ldq, float* S, cce_stream_t stream) {
+  cce_status s = check_matrix(X, x_dtype, M, D, ldx);
+  if (s == CCE_OK) s = check_codes(Q, ldq, S, D);
+  if (s != CCE_OK) return s;
+  if (D > kMaxQuantD) return CCE_ERR_UNSUPPORTED;
+  const int G = int(ceil_div(D, QGROUP));
+  const int grid = int(std::min<int64_t>(ceil_div(M * G, 16), 16 * sm_count_guess()));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(PK_QUANT, st);
+  const bool vec = D % 8 == 0 && rows16(X, ldx, dtype_bytes(x_dtype)) && codes8(Q, ldq);
+  with_type(x_dtype, [&](auto t) {
+    using T = typename decltype(t)::type;
+    with_bool(vec, [&](auto v) {
+      quant_rows_kernel<decltype(v)::value, T><<<grid, 256, 0, st>>>(
+          static_cast<const T*>(X), ldx, M, int(D), G, qmat(Q, ldq, S, D));
+    });
+  });
+  return launch_ok();
+}
+
+cce_status cce_fp8_quant_blocks(const void* W, cce_dtype w_dtype, int64_t N, int64_t K,
+                                int64_t ldw, uint8_t* Q, int64_t ldq, float* S,
+                                cce_stream_t stream) {
+  cce_status s = check_matrix(W, w_dtype, N, K, ldw);
+  if (s == CCE_OK) s = check_codes(Q, ldq, S, K);
+  if (s != CCE_OK) return s;
+  if (K > kMaxQuantD || ceil_div(N, QGROUP) > 65535) return CCE_ERR_UNSUPPORTED;
+  const dim3 grid(unsigned(ceil_div(K, QGROUP)), unsigned(ceil_div(N, QGROUP)));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(PK_QUANT, st);
+  const bool vec = K % 8 == 0 && rows16(W, ldw, dtype_bytes(w_dtype)) && codes8(Q, ldq);
+  with_type(w_dtype, [&](auto t) {
+    using T = typename decltype(t)::type;
+    with_bool(vec, [&](auto v) {
+      quant_blocks_kernel<decltype(v)::value, T><<<grid, 256, 0, st>>>(
+          static_cast<const T*>(W), ldw, N, int(K), qmat(Q, ldq, S, K));
+    });
+  });
+  return launch_ok();
+}
+
+cce_status cce_norm_forward(const void* X, cce_dtype x_dtype, int64_t M, int64_t D, int64_t ldx,
+                            const void* w, cce_dtype w_dtype, double eps, void* H,
+                            cce_dtype h_dtype, int64_t ldh, uint8_t* H8, int64_t ldh8, float* Hs,
+                            uint8_t* X8, int64_t ldx8, float* Xs, float* rstd,
+                            cce_stream_t stream) {
+  cce_status s = check_matrix(X, x_dtype, M, D, ldx);
+  if (s == CCE_OK) s = check_matrix(w, w_dtype, 1, D, D);
+  if (s == CCE_OK && H != nullptr) s = check_matrix(H, h_dtype, M, D, ldh);
+  if (s == CCE_OK && (H8 != nullptr || Hs != nullptr)) s = check_codes(H8, ldh8, Hs, D);
+  if (s == CCE_OK && (X8 != nullptr || Xs != nullptr)) s = check_codes(X8, ldx8, Xs, D);
+  if (s != CCE_OK) return s;
+  if (!(eps >= 0.0) || eps > 1e30 || (rstd != nullptr && !aligned_to(rstd, 4)) ||
+      (H == nullptr && H8 == nullptr && X8 == nullptr && rstd == nullptr))
+    return CCE_ERR_INVALID_ARGUMENT;
+  if (D > kMaxNormD) return CCE_ERR_UNSUPPORTED;
+  NormFwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x = X;
+  a.ldx = ldx;
+  a.w = w;
+  a.w_bf16 = w_dtype == CCE_BF16;
+  a.M = M;
+  a.D = int(D);
+  a.eps = float(eps);
+  a.h = H;
+  a.ldh = ldh;
+  const bool vec = D % 8 == 0 && rows16(X, ldx, dtype_bytes(x_dtype)) && aligned_to(w, 16) &&
+                   (H == nullptr || rows16(H, ldh, dtype_bytes(h_dtype))) &&
+                   (H8 == nullptr || codes8(H8, ldh8)) && (X8 == nullptr || codes8(X8, ldx8));
+  if (H8 != nullptr) a.h8 = qmat(H8, ldh8, Hs, D);
+  if (X8 != nullptr) a.x8 = qmat(X8, ldx8, Xs, D);
+  a.rstd = rstd;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(PK_NORM, st);
+  with_type(x_dtype, [&](auto tx) {
+    with_type(H != nullptr ? h_dtype : CCE_BF16, [&](auto th) {
+      with_bool(vec, [&](auto v) {
+        with_team<decltype(v)::value>(D, [&](auto tpr, auto r) {
+          constexpr int T = decltype(tpr)::value, B = norm_block(T);
+          const int grid = int(std::min<int64_t>(ceil_div(M, B / T), 32 * sm_count_guess()));
+          norm_fwd_kernel<decltype(v)::value, typename decltype(tx)::type,
+                          typename decltype(th)::type, T, decltype(r)::value>
+              <<<grid, B, 0, st>>>(a);
+        });
+      });
+    });
+  });
+  return launch_ok();
+}
+
+size_t cce_norm_backward_workspace_bytes(int64_t M, int64_t D) {
+  if (M <= 0 || D <= 0 || M > kMaxRows || D > kMaxNormD) return 0;
+  return kStatusBytes + size_t(norm_bwd_blocks(M, D)) * size_t(D) * 4;
+}
+
+cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs, const float* rstd,
+                             int64_t M, int64_t D, const void* w, cce_dtype w_dtype,
+                             const void* dH, cce_dtype dh_dtype, int64_t lddh, void* dX,
+                             cce_dtype dx_dtype, int64_t lddx, float* dW, void* ws,
+                             size_t ws_bytes, cce_stream_t stream) {
+  cce_status s = check_matrix(dH, dh_dtype, M, D, lddh);
+  if (s == CCE_OK) s = check_matrix(dX, dx_dtype, M, D, lddx);
+  if (s == CCE_OK) s = check_matrix(w, w_dtype, 1, D, D);
+  if (s == CCE_OK) s = check_codes(X8, ldx8, Xs, D);
+  if (s != CCE_OK) return s;
+  if (rstd == nullptr || !aligned_to(rstd, 4)) return CCE_ERR_INVALID_ARGUMENT;
+  if (D > kMaxNormD) return CCE_ERR_UNSUPPORTED;
+  if (dW != nullptr) {
+    if (ws == nullptr || !aligned16(ws) || !aligned_to(dW, 4)) return CCE_ERR_INVALID_ARGUMENT;
+    if (ws_bytes < cce_norm_backward_workspace_bytes(M, D)) return CCE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  NormBwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.x8 = qmat(X8, ldx8, Xs, D);
+  a.rstd = rstd;
+  a.w = w;
+  a.w_bf16 = w_dtype == CCE_BF16;
+  a.dh = dH;
+  a.lddh = lddh;
+  a.M = M;
+  a.D = int(D);
+  a.dx = dX;
+  a.lddx = lddx;
+  const bool vec = D % 8 == 0 && rows16(dH, lddh, dtype_bytes(dh_dtype)) &&
+                   rows16(dX, lddx, dtype_bytes(dx_dtype)) && aligned_to(w, 16) &&
+                   codes8(X8, ldx8);
+  if (dW != nullptr)
+    a.dw_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+  const int grid = norm_bwd_blocks(M, D);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(PK_NORM, st);
+  with_type(dx_dtype, [&](auto tx) {
+    with_type(dh_dtype, [&](auto th) {
+      with_bool(vec, [&](auto v) {
+        with_team<decltype(v)::value>(D, [&](auto tpr, auto r) {
+          constexpr int T = decltype(tpr)::value;
+          norm_bwd_kernel<decltype(v)::value, typename decltype(tx)::type,
+                          typename decltype(th)::type, T, decltype(r)::value>
+              <<<grid, norm_block(T), 0, st>>>(a);
+        });
+      });
+    });
+  });
+  if (launch_ok() != CCE_OK) return CCE_ERR_CUDA;
+  if (dW != nullptr)
+    norm_dw_kernel<<<unsigned(ceil_div(D, 32)), 256, 0, st>>>(a.dw_part, grid, int(D), dW);
+  return launch_ok();
+}
+
+}  // extern "C"

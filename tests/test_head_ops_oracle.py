@@ -1,0 +1,108 @@
+"""Pins of the oracle of the operators around the head, and the refusals that
+need no GPU."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from lm_head_cross_flash_b200 import build, cce
+from oracle import head_ops as O
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return cce.lib()
+
+
+def test_e4m3_round_matches_the_type():
+    """Every e4m3 value is a fixed point, and rounding agrees with torch's
+    cast (nearest, ties to even) inside the range."""
+    every = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    fin = every[np.isfinite(every)]
+    assert np.array_equal(O.e4m3_round(fin), fin)
+    r = np.random.default_rng(0)
+    v = np.concatenate([r.uniform(-448, 448, 20000), r.uniform(-0.05, 0.05, 20000),
+                        (np.sort(fin)[1:] + np.sort(fin)[:-1]) / 2]).astype(np.float32)
+    assert np.array_equal(O.e4m3_round(v), torch.from_numpy(v).to(torch.float8_e4m3fn).double().numpy())
+    assert O.e4m3_round(1e9) == 448 and O.e4m3_round(-np.inf) == -448
+
+
+def test_quantised_values_stay_within_half_a_step():
+    x = np.random.default_rng(1).standard_normal((7, 300)).astype(np.float32)
+    for q, v in ((O.quant_rows(x), O.rows_values), (O.quant_blocks(x), O.blocks_values)):
+        got = v(*q)
+        m = np.abs(x).max()
+        assert (np.abs(got - x) <= np.maximum(np.abs(x) * 2.0 ** -4, m / 448 * 2.0 ** -10) * 1.0001).all()
+
+
+def test_norm_gradient_is_the_slope():
+    r = np.random.default_rng(2)
+    x, w, dh = r.standard_normal((3, 50)), r.standard_normal(50), r.standard_normal((3, 50))
+    h, rstd = O.norm_forward(x, w, 1e-3)
+    dx, dw = O.norm_backward(x * rstd[:, None], rstd, w, dh)
+    v, vw, e = r.standard_normal(x.shape), r.standard_normal(50), 1e-6
+    f = lambda a, b: (dh * O.norm_forward(x + a * v, w + b * vw, 1e-3)[0]).sum()
+    assert abs((f(e, 0) - f(-e, 0)) / (2 * e) - (dx * v).sum()) < 1e-7
+    assert abs((f(0, e) - f(0, -e)) / (2 * e) - (dw * vw).sum()) < 1e-7
+
+
+P = 1 << 20  # an aligned address; refused calls never touch it
+
+
+def test_quant_refusals(lib):
+    for f in (lib.cce_fp8_quant_rows, lib.cce_fp8_quant_blocks):
+        bad = [(None, 1, 8, 128, 128, P, 128, P), (P, 1, 0, 128, 128, P, 128, P),
+               (P, 1, 8, 0, 128, P, 128, P), (P, 1, 8, 128, 127, P, 128, P),
+               (P, 1, 8, 128, 128, None, 128, P), (P, 1, 8, 128, 128, P, 127, P),
+               (P, 1, 8, 128, 128, P, 128, None), (P, 7, 8, 128, 128, P, 128, P),
+               (P + 1, 1, 8, 128, 128, P, 128, P), (P + 2, 0, 8, 128, 128, P, 128, P),
+               (P, 1, 8, 128, 128, P, 128, P + 2)]
+        for a in bad:
+            assert f(*a, None) == 1, a
+        assert f(P, 1, 8, 65537, 65537, P, 65537, P, None) == 2
+        assert f(P, 1, (1 << 30) + 1, 8, 8, P, 8, P, None) == 2
+    assert lib.cce_fp8_quant_blocks(P, 1, 65535 * 128 + 1, 8, 8, P, 8, P, None) == 2
+
+
+def test_norm_refusals(lib):
+    ok = dict(X=P, xt=1, M=4, D=256, ldx=256, w=P, wt=0, eps=1e-6, H=P, ht=1, ldh=256, H8=None,
+              ldh8=0, Hs=None, X8=None, ldx8=0, Xs=None, rstd=None, stream=None)
+
+    def call(**kw):
+        return lib.cce_norm_forward(*{**ok, **kw}.values())
+
+    for kw in (dict(X=None), dict(w=None), dict(M=0), dict(D=-1), dict(ldx=255), dict(ldh=255),
+               dict(xt=2), dict(wt=-1), dict(ht=5), dict(eps=-1.0), dict(eps=float("nan")),
+               dict(H=None), dict(H8=P, ldh8=256), dict(Hs=P), dict(X8=P, ldx8=255, Xs=P),
+               dict(rstd=P + 1), dict(X=P + 1), dict(w=P + 2)):
+        assert call(**kw) == 1, kw
+    assert call(D=16385, ldx=16385, ldh=16385) == 2
+    okb = dict(X8=P, ldx8=256, Xs=P, rstd=P, M=4, D=256, w=P, wt=0, dH=P, dht=0, lddh=256, dX=P,
+               dxt=1, lddx=256, dW=P, ws=P, n=1 << 20, stream=None)
+
+    def back(**kw):
+        return lib.cce_norm_backward(*{**okb, **kw}.values())
+
+    for kw in (dict(X8=None), dict(Xs=None), dict(rstd=None), dict(w=None), dict(dH=None),
+               dict(dX=None), dict(ws=None), dict(ws=P + 8), dict(M=0), dict(lddh=1),
+               dict(lddx=255), dict(ldx8=0), dict(dht=3), dict(dxt=3), dict(dW=P + 2)):
+        assert back(**kw) == 1, kw
+    assert back(D=16385, lddh=16385, lddx=16385, ldx8=16385) == 2
+    need = lib.cce_norm_backward_workspace_bytes(4, 256)
+    assert need > 256 and back(n=need - 1) == 4
+    assert lib.cce_norm_backward_workspace_bytes(0, 256) == 0
+    assert lib.cce_norm_backward_workspace_bytes(4, 16385) == 0
+
+
+def test_binding_refuses_what_the_library_would_misread():
+    cpu = torch.zeros(4, 128)
+    with pytest.raises(ValueError, match="CUDA"):
+        cce.cce_fp8_quant_rows(cpu, cpu, cpu)
+    with pytest.raises(ValueError, match="CUDA"):
+        cce.cce_norm_forward(cpu, cpu[0], 1e-6, H=cpu)
+    with pytest.raises(ValueError, match="CUDA"):
+        cce.cce_norm_backward(cpu, cpu, cpu, cpu, cpu, cpu)
+    assert cce.fp8_groups(1) == 1 and cce.fp8_groups(128) == 1 and cce.fp8_groups(129) == 2
