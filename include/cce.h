@@ -508,8 +508,8 @@ cce_status cce_forward_noalloc(const void* H, int64_t M, const cce_head* W,
                                uint32_t* status, cce_stream_t stream);
 
 /* ==========================================================================
- * Operators around the head: 8-bit rows and weights, the final norm with an
- * 8-bit checkpoint of its input.
+ * Operators around the head: 8-bit rows and weights and their product, the
+ * final norm with an 8-bit checkpoint of its input.
  *
  * The conventions at the top of this file hold, with these additions:
  * - Matrices are row-major; ldX is the distance of two rows, in elements
@@ -541,6 +541,23 @@ cce_status cce_fp8_quant_rows(const void* X, cce_dtype x_dtype, int64_t M,
 cce_status cce_fp8_quant_blocks(const void* W, cce_dtype w_dtype, int64_t N,
                                 int64_t K, int64_t ldw, uint8_t* Q,
                                 int64_t ldq, float* S, cce_stream_t stream);
+
+/*
+ * Product of 8-bit rows A [M, K] (row groups, SA [M, ceil(K/128)]) and an
+ * 8-bit head B [N, K] (128 x 128 blocks, SB [ceil(N/128), ceil(K/128)]), the
+ * logits that cce_sample_rows reads:
+ *   C[m,n] = sum_g SA[m,g] SB[n/128,g] sum_{k in g} A[m,k] B[n,k]
+ * C: [M, N], f32 or bf16, summed in fp32 and rounded once.  Every group's sum
+ * is made on the tensor cores; the scales are applied in fp32.
+ * A and B: 16-byte aligned, lda and ldb multiples of 16 (bytes; not looked at
+ * for a single row).  K <= 65,536.  The first 256 bytes of ws hold the status
+ * word (zeroed once before first use); no more is used.
+ */
+cce_status cce_fp8_matmul(const uint8_t* A, int64_t lda, const float* SA,
+                          const uint8_t* B, int64_t ldb, const float* SB,
+                          int64_t M, int64_t N, int64_t K, void* C,
+                          cce_dtype c_dtype, int64_t ldc, void* ws,
+                          size_t ws_bytes, cce_stream_t stream);
 
 /*
  * Final norm, the step that makes the head's rows from the residual stream:

@@ -136,6 +136,11 @@ _SIGS = {
     "cce_fp8_quant_blocks": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                             ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                             ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "cce_fp8_matmul": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                      ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                      ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                      ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "cce_norm_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                         ctypes.c_int, ctypes.c_double, ctypes.c_void_p,
@@ -647,6 +652,21 @@ def cce_fp8_quant_blocks(W, Q, S, stream=None):
     q, _, ldq = _mat("Q", Q, _CODES, N, K, dev)
     _run("cce_fp8_quant_blocks", dev, stream, x, xt, N, K, ldx, q, ldq,
          _dense("S", S, _F32, (fp8_groups(N), fp8_groups(K)), dev))
+
+
+def cce_fp8_matmul(A, SA, B, SB, C, ws, stream=None):
+    """C [M, N] (f32 or bf16) = rows A [M, K] (scales SA, one for each 128
+    columns) times head B [N, K] (scales SB, one for each 128 x 128 block),
+    transposed.  A and B: rows on 16-byte boundaries (``fp8_empty``); ``ws``:
+    uint8, 256 bytes for the status word, zeroed once."""
+    (M, N), K, dev = C.shape, A.shape[1], C.get_device()
+    c, ct, ldc = _mat("C", C, _MAT_TYPES, M, N, dev)
+    a, _, lda = _mat("A", A, _CODES, M, K, dev)
+    b, _, ldb = _mat("B", B, _CODES, N, K, dev)
+    G = fp8_groups(K)
+    _run("cce_fp8_matmul", dev, stream, a, lda, _dense("SA", SA, _F32, (M, G), dev), b, ldb,
+         _dense("SB", SB, _F32, (fp8_groups(N), G), dev), M, N, K, c, ct, ldc,
+         *_workspace(ws, dev))
 
 
 def _codes_of(name, q, s, M, D, dev):

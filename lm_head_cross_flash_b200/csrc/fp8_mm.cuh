@@ -1,0 +1,528 @@
+// fp8_mm.cuh — the product of 8-bit rows and an 8-bit head,
+//   C[m,n] = sum_g sa[m,g] sb[n/128,g] sum_{k in group g} a[m,k] b[n,k],
+// on the 8-bit tensor-core path (tcgen05.mma.kind::f8f6f4, e4m3 operands,
+// fp32 accumulation).
+//
+// The scales differ from one group of 128 to the next, so a group's partial
+// sum (4 MMAs of K = 32) is taken out of tensor memory and added, times its
+// scales, to fp32 sums in registers.  That costs one tensor-memory read and
+// one FMA per partial; both run beside the next group's MMAs.
+//
+// fp8_rows_kernel: any number of rows; 128 rows x 256 columns of C per CTA,
+//   row tiles fastest, so the CTAs in flight share the same rows of b.
+// fp8_few_kernel: up to 128 rows (decoding).  The roles of the operands are
+//   exchanged: 128 rows of b are the MMA's M side and the few rows of a its N
+//   side, so a pass over b costs no idle tensor rows; the CTAs of a cluster
+//   split the groups where the head has too few rows to fill the SMs.
+#pragma once
+
+#include "row_ops.cuh"
+
+namespace cce {
+
+// kind::f8f6f4, e4m3 x e4m3, fp32 accumulator, both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+__device__ __forceinline__ void umma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 lanes x 16 consecutive fp32 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// tcgen05.wait::ld that names the registers it waits for.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+struct Fp8Args {
+  int M, N;
+  int G;  // groups of K
+  const float* sa;  // [M, G]
+  const float* sb;  // [ceil(N/128), G]
+  void* c;
+  int64_t ldc;
+  int c_bf16;
+  int vec;         // rows of c start on 16-byte boundaries
+  int n_rt, n_ct;  // row and column tiles
+  int group_rt;    // row tiles per raster group
+  uint64_t wait_ns;
+  uint32_t* status;
+};
+
+// Barriers and flags at the end of shared memory.
+template <int NST, int NBUF>
+struct Fp8Sync {
+  uint64_t full[NST], empty[NST];
+  uint64_t acc_full[NBUF], acc_empty[NBUF];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+};
+
+// Every copy that was issued lands before the CTA may exit.
+template <int NST>
+__device__ __forceinline__ void drain_copies(uint64_t* full, uint32_t mask, uint32_t phases) {
+  for (int s = 0; s < NST; ++s)
+    if (mask & (1u << s)) wait_bounded(&full[s], (phases >> s) & 1u, 1000000000ull, nullptr);
+}
+
+// ----------------------------------------------------------- many rows --
+constexpr int F8_BM = 128, F8_BN = 256, F8_BK = 128;
+constexpr int F8_STAGES = 4;
+constexpr int F8_STAGE = (F8_BM + F8_BN) * F8_BK;
+constexpr int F8_THREADS = 320;  // copies, MMA, 8 epilogue warps
+using F8Sync = Fp8Sync<F8_STAGES, 2>;
+constexpr int F8_SMEM = F8_STAGES * F8_STAGE + sizeof(F8Sync) + 1024;
+
+__global__ void __launch_bounds__(F8_THREADS, 1)
+    fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA,
+                    const __grid_constant__ CUtensorMap tmB, Fp8Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  F8Sync* sy = reinterpret_cast<F8Sync*>(base + F8_STAGES * F8_STAGE);
+  volatile int* abort_flag = &sy->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ntiles = a.n_rt * a.n_ct;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < F8_STAGES; ++s) {
+      mbar_init(&sy->full[s], 1);
+      mbar_init(&sy->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sy->acc_full[b], 1);
+      mbar_init(&sy->acc_empty[b], 8);
+    }
+    mbar_init(&sy->drain, 1);
+    sy->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sy->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sy->tmem;
+
+  auto tile_at = [&](int t, int& rt, int& ct) {
+    const int per_group = a.group_rt * a.n_ct;
+    const int grp = t / per_group, r = t - grp * per_group;
+    const int g0 = grp * a.group_rt, gn = min(a.group_rt, a.n_rt - g0);
+    rt = g0 + r % gn;
+    ct = r / gn;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, mask = 0, phases = 0;
+      bool ok = true;
+      const uint64_t keep = l2_policy_evict_last();
+      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+        int rt, ct;
+        tile_at(t, rt, ct);
+        for (int g = 0; g < a.G; ++g) {
+          if (!wait_bounded(&sy->empty[stage], phase ^ 1u, a.wait_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* s = base + stage * F8_STAGE;
+          mbar_arrive_expect_tx(&sy->full[stage], F8_STAGE);
+          tma_load_2d_hint(s, &tmA, &sy->full[stage], g * F8_BK, rt * F8_BM, keep);
+          tma_load_2d(s + F8_BM * F8_BK, &tmB, &sy->full[stage], g * F8_BK, ct * F8_BN);
+          mask |= 1u << stage;
+          phases = (phases & ~(1u << stage)) | (phase << stage);
+          if (++stage == F8_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        set_status(a.status, ST_TIMEOUT);
+        *abort_flag = 1;
+      }
+      drain_copies<F8_STAGES>(sy->full, mask, phases);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(F8_BM, F8_BN);
+      int stage = 0;
+      uint32_t phase = 0, acc = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+        for (int g = 0; g < a.G; ++g, ++acc) {
+          const int b = acc & 1;
+          if (!wait_bounded(&sy->acc_empty[b], ((acc >> 1) & 1) ^ 1u, a.wait_ns, abort_flag) ||
+              !wait_bounded(&sy->full[stage], phase, a.wait_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sA = smem_u32(base + stage * F8_STAGE), sB = sA + F8_BM * F8_BK;
+#pragma unroll
+          for (int j = 0; j < F8_BK / 32; ++j)
+            umma_e4m3_ss(tmem + b * F8_BN, sdesc_sw128(sA + j * 32, 16, 1024),
+                         sdesc_sw128(sB + j * 32, 16, 1024), idesc, j != 0);
+          umma_commit(&sy->empty[stage]);
+          umma_commit(&sy->acc_full[b]);
+          if (++stage == F8_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        set_status(a.status, ST_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // the MMAs of this thread complete before tensor memory is released
+      umma_commit(&sy->drain);
+      wait_bounded(&sy->drain, 0, 1000000000ull, nullptr);
+    }
+  } else {
+    // One row of C and 128 of its columns per thread.
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+    uint32_t acc = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      int rt, ct;
+      tile_at(t, rt, ct);
+      const int row = rt * F8_BM + quad * 32 + lane, col = ct * F8_BN + half * 128;
+      const float* psa = a.sa + static_cast<size_t>(min(row, a.M - 1)) * a.G;
+      const float* psb = a.sb + static_cast<size_t>(min(col, a.N - 1) / QGROUP) * a.G;
+      float c[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) c[j] = 0.f;
+      float sc = __ldg(psa) * __ldg(psb);
+      for (int g = 0; g < a.G; ++g, ++acc) {
+        const int b = acc & 1;
+        const float s = sc;
+        const int gn = min(g + 1, a.G - 1);
+        sc = __ldg(psa + gn) * __ldg(psb + gn);
+        if (!wait_bounded(&sy->acc_full[b], (acc >> 1) & 1, a.wait_ns, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t r[2][16];
+        tmem_ld16(taddr + b * F8_BN, r[0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          tmem_ld_wait16(r[i & 1]);
+          if (i < 7) tmem_ld16(taddr + b * F8_BN + (i + 1) * 16, r[(i + 1) & 1]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            c[i * 16 + j] = fmaf(__uint_as_float(r[i & 1][j]), s, c[i * 16 + j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sy->acc_empty[b]);
+      }
+      if (!ok) {
+        if (lane == 0) {
+          set_status(a.status, ST_TIMEOUT);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      if (row < a.M) {
+        const bool vec = a.vec && col + 128 <= a.N;
+        if (a.c_bf16) {
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.c) + row * a.ldc + col;
+          if (vec) {
+#pragma unroll
+            for (int j = 0; j < 128; j += 8)
+              store8<true>(out, j, 128, *reinterpret_cast<const float(*)[8]>(&c[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+              if (col + j < a.N) out[j] = __float2bfloat16_rn(c[j]);
+          }
+        } else {
+          float* out = static_cast<float*>(a.c) + row * a.ldc + col;
+          if (vec) {
+#pragma unroll
+            for (int j = 0; j < 128; j += 8)
+              store8<true>(out, j, 128, *reinterpret_cast<const float(*)[8]>(&c[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 128; ++j)
+              if (col + j < a.N) out[j] = c[j];
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------- few rows --
+// NP: rows of a, padded (16, 32, 64, 128).  A stage holds 128 rows of b and
+// the NP rows of a for one group; four accumulators of NP columns.
+constexpr int FF_MAX_SCALES = 8192;  // NP * groups per CTA, kept in shared memory
+template <int NP>
+struct FfCfg {
+  static constexpr int STAGE = (128 + NP) * 128;
+  static constexpr int SCALES = FF_MAX_SCALES * 4;
+  static constexpr int NST = (NP <= 64 ? 160 : 176) * 1024 / STAGE;
+  static constexpr int NBUF = 4;
+  static constexpr int COLS = NBUF * NP < 32 ? 32 : NBUF * NP;
+  static constexpr int HALVES = NP >= 64 ? 2 : 1;  // warps that share a lane quarter
+  static constexpr int NC = NP / HALVES;           // columns per thread
+  static constexpr int THREADS = 64 + HALVES * 128;
+  using Sync = Fp8Sync<NST, NBUF>;
+  static constexpr int SMEM = NST * STAGE + SCALES + int(sizeof(Sync)) + 1024;
+  static_assert(NST * STAGE >= 128 * NP * 4, "the stages hold a tile's sums");
+};
+
+// One tile of 128 rows of b per cluster and round; CTA `rank` of the cluster
+// takes the groups [rank*G/S, (rank+1)*G/S).  With S > 1 every cluster has one
+// tile, and the CTAs' sums meet in shared memory: each CTA adds one share of
+// the columns over all of them, in the order of the ranks.
+template <int NP>
+__global__ void __launch_bounds__(FfCfg<NP>::THREADS, 1)
+    fp8_few_kernel(const __grid_constant__ CUtensorMap tmA,
+                   const __grid_constant__ CUtensorMap tmB, Fp8Args a, int S) {
+  using C = FfCfg<NP>;
+  constexpr int NST = C::NST, NBUF = C::NBUF, NC = C::NC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* scales = reinterpret_cast<float*>(base + NST * C::STAGE);  // [groups, NP]
+  typename C::Sync* sy = reinterpret_cast<typename C::Sync*>(base + NST * C::STAGE + C::SCALES);
+  volatile int* abort_flag = &sy->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = S > 1 ? int(cluster_ctarank()) : 0;
+  const int tile0 = S > 1 ? int(blockIdx.x) / S : int(blockIdx.x);
+  const int tstep = S > 1 ? a.n_ct : int(gridDim.x);
+  const int g0 = rank * a.G / S, ng = (rank + 1) * a.G / S - g0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sy->full[s], 1);
+      mbar_init(&sy->empty[s], 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(&sy->acc_full[b], 1);
+      mbar_init(&sy->acc_empty[b], C::HALVES * 4);
+    }
+    mbar_init(&sy->drain, 1);
+    sy->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sy->tmem, C::COLS);
+    tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < ng * NP; i += C::THREADS) {
+    const int m = i / ng, g = i - m * ng;
+    scales[g * NP + m] = m < a.M ? __ldg(a.sa + static_cast<size_t>(m) * a.G + g0 + g) : 0.f;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sy->tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, mask = 0, phases = 0;
+      bool ok = true;
+      const uint64_t keep = l2_policy_evict_last(), stream = l2_policy_evict_first();
+      for (int t = tile0; t < a.n_ct && ok; t += tstep) {
+        for (int g = 0; g < ng; ++g) {
+          if (!wait_bounded(&sy->empty[stage], phase ^ 1u, a.wait_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* s = base + stage * C::STAGE;
+          mbar_arrive_expect_tx(&sy->full[stage], C::STAGE);
+          tma_load_2d_hint(s, &tmB, &sy->full[stage], (g0 + g) * 128, t * 128, stream);
+          tma_load_2d_hint(s + 128 * 128, &tmA, &sy->full[stage], (g0 + g) * 128, 0, keep);
+          mask |= 1u << stage;
+          phases = (phases & ~(1u << stage)) | (phase << stage);
+          if (++stage == NST) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        set_status(a.status, ST_TIMEOUT);
+        *abort_flag = 1;
+      }
+      drain_copies<NST>(sy->full, mask, phases);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(128, NP);
+      int stage = 0;
+      uint32_t phase = 0, acc = 0;
+      bool ok = true;
+      for (int t = tile0; t < a.n_ct && ok; t += tstep) {
+        for (int g = 0; g < ng; ++g, ++acc) {
+          const int b = acc % NBUF;
+          if (!wait_bounded(&sy->acc_empty[b], ((acc / NBUF) & 1) ^ 1u, a.wait_ns, abort_flag) ||
+              !wait_bounded(&sy->full[stage], phase, a.wait_ns, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sB = smem_u32(base + stage * C::STAGE), sA = sB + 128 * 128;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            umma_e4m3_ss(tmem + b * NP, sdesc_sw128(sB + j * 32, 16, 1024),
+                         sdesc_sw128(sA + j * 32, 16, 1024), idesc, j != 0);
+          umma_commit(&sy->empty[stage]);
+          umma_commit(&sy->acc_full[b]);
+          if (++stage == NST) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        set_status(a.status, ST_TIMEOUT);
+        *abort_flag = 1;
+      }
+      umma_commit(&sy->drain);
+      wait_bounded(&sy->drain, 0, 1000000000ull, nullptr);
+    }
+  } else {
+    // One row of b (one column of C) and NC rows of C per thread.
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int vrow = quad * 32 + lane;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * NC;
+    uint32_t acc = 0;
+    bool ok = true;
+    for (int t = tile0; t < a.n_ct && ok; t += tstep) {
+      const float* psb = a.sb + static_cast<size_t>(t) * a.G + g0;
+      float c[NC];
+#pragma unroll
+      for (int j = 0; j < NC; ++j) c[j] = 0.f;
+      float nb = ng > 0 ? __ldg(psb) : 0.f;
+      for (int g = 0; g < ng; ++g, ++acc) {
+        const int b = acc % NBUF;
+        const float sb = nb;
+        nb = __ldg(psb + min(g + 1, ng - 1));
+        if (!wait_bounded(&sy->acc_full[b], (acc / NBUF) & 1, a.wait_ns, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float4* sg = reinterpret_cast<const float4*>(scales + g * NP + half * NC);
+        uint32_t r[NC / 16][16];
+#pragma unroll
+        for (int i = 0; i < NC / 16; ++i) tmem_ld16(taddr + b * NP + i * 16, r[i]);
+#pragma unroll
+        for (int i = 0; i < NC / 16; ++i) {
+          tmem_ld_wait16(r[i]);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const float4 s = sg[i * 4 + j / 4];
+            c[i * 16 + j] = fmaf(__uint_as_float(r[i][j]), s.x * sb, c[i * 16 + j]);
+            c[i * 16 + j + 1] = fmaf(__uint_as_float(r[i][j + 1]), s.y * sb, c[i * 16 + j + 1]);
+            c[i * 16 + j + 2] = fmaf(__uint_as_float(r[i][j + 2]), s.z * sb, c[i * 16 + j + 2]);
+            c[i * 16 + j + 3] = fmaf(__uint_as_float(r[i][j + 3]), s.w * sb, c[i * 16 + j + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sy->acc_empty[b]);
+      }
+      if (!ok) {
+        if (lane == 0) {
+          set_status(a.status, ST_TIMEOUT);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      if (S == 1) {
+        const int n = t * 128 + vrow;
+        if (n < a.N) {
+#pragma unroll
+          for (int j = 0; j < NC; ++j) {
+            const int m = half * NC + j;
+            if (m < a.M) {
+              if (a.c_bf16)
+                static_cast<__nv_bfloat16*>(a.c)[m * a.ldc + n] = __float2bfloat16_rn(c[j]);
+              else
+                static_cast<float*>(a.c)[m * a.ldc + n] = c[j];
+            }
+          }
+        }
+      } else {
+        // the stages are free: all of this CTA's MMAs have been waited for
+        float* part = reinterpret_cast<float*>(base);
+#pragma unroll
+        for (int j = 0; j < NC; ++j) part[(half * NC + j) * 128 + vrow] = c[j];
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (S > 1) {
+    cluster_sync_all();
+    const uint32_t part = smem_u32(base);
+    const int m0 = rank * NP / S, m1 = (rank + 1) * NP / S;
+    for (int i = threadIdx.x; i < (m1 - m0) * 128; i += C::THREADS) {
+      const int m = m0 + (i >> 7), v = i & 127, n = tile0 * 128 + v;
+      float s = 0.f;
+      for (int r = 0; r < S; ++r) {
+        float x;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                     : "=f"(x)
+                     : "r"(mapa_shared(part + (m * 128 + v) * 4, r))
+                     : "memory");
+        s += x;
+      }
+      if (m < a.M && n < a.N) {
+        if (a.c_bf16)
+          static_cast<__nv_bfloat16*>(a.c)[m * a.ldc + n] = __float2bfloat16_rn(s);
+        else
+          static_cast<float*>(a.c)[m * a.ldc + n] = s;
+      }
+    }
+    cluster_sync_all();  // the sums stay until every CTA has read them
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::COLS);
+  }
+}
+
+}  // namespace cce

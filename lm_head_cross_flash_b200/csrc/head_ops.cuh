@@ -3,6 +3,7 @@
 // behind the helpers it shares with the head's own entry points.
 #pragma once
 
+#include "fp8_mm.cuh"
 #include "row_ops.cuh"
 
 namespace {
@@ -85,6 +86,64 @@ int norm_bwd_blocks(int64_t M, int64_t D) {
   with_team<true>(D, [&](auto tpr, auto) { rpb = norm_block(tpr()) / tpr(); });
   const int64_t per_sm = D > 256 * 8 ? 2 : 4;
   return int(std::max<int64_t>(1, std::min<int64_t>(ceil_div(M, rpb), per_sm * sm_count_guess())));
+}
+
+// 8-bit matrix [rows, K] in boxes of one group by `box_rows` rows; bytes
+// behind K are not read (zero fill).
+bool make_fp8_map(CUtensorMap* m, const void* p, int64_t rows, int64_t K, int64_t ld,
+                  uint32_t box_rows) {
+  const uint64_t dims[2] = {uint64_t(K), uint64_t(rows)};
+  const uint64_t strides[1] = {uint64_t(ld)};
+  const uint32_t box[2] = {QGROUP, box_rows};
+  return make_map_ex(m, p, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, dims, strides, box,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <typename K>
+cce_status set_smem_once(K kernel, int bytes, bool (&done)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CCE_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  if (!done[dev] && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         bytes) != cudaSuccess)
+    return CCE_ERR_CUDA;
+  done[dev] = true;
+  return CCE_OK;
+}
+
+// Few rows: CTAs per tile of 128 head rows, a power of two up to 8, as many
+// as still run at once (a head of 4,096 rows has 32 tiles for 148 SMs).
+int few_split(int64_t tiles, int64_t G, int sms) {
+  int s = 1;
+  while (s < 8 && 2 * s * tiles <= sms && 2 * s <= G) s *= 2;
+  return s;
+}
+
+template <int NP>
+cce_status launch_few(const void* A, int64_t lda, const void* B, int64_t ldb, int64_t K, int S,
+                      int sms, const Fp8Args& args, cudaStream_t st) {
+  static bool done[64];
+  using C = FfCfg<NP>;
+  const cce_status s = set_smem_once(fp8_few_kernel<NP>, C::SMEM, done);
+  if (s != CCE_OK) return s;
+  CUtensorMap ma, mb;
+  if (!make_fp8_map(&ma, A, args.M, K, lda, NP) || !make_fp8_map(&mb, B, args.N, K, ldb, 128))
+    return CCE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(S > 1 ? unsigned(args.n_ct * S) : unsigned(std::min(args.n_ct, sms)));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(S);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = S > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fp8_few_kernel<NP>, ma, mb, args, S) == cudaSuccess
+             ? launch_ok()
+             : (cudaGetLastError(), CCE_ERR_CUDA);
 }
 
 }  // namespace
@@ -239,6 +298,70 @@ cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs, c
   if (launch_ok() != CCE_OK) return CCE_ERR_CUDA;
   if (dW != nullptr)
     norm_dw_kernel<<<unsigned(ceil_div(D, 32)), 256, 0, st>>>(a.dw_part, grid, int(D), dW);
+  return launch_ok();
+}
+
+cce_status cce_fp8_matmul(const uint8_t* A, int64_t lda, const float* SA, const uint8_t* B,
+                          int64_t ldb, const float* SB, int64_t M, int64_t N, int64_t K, void* C,
+                          cce_dtype c_dtype, int64_t ldc, void* ws, size_t ws_bytes,
+                          cce_stream_t stream) {
+  cce_status s = check_matrix(C, c_dtype, M, N, ldc);
+  if (s != CCE_OK) return s;
+  if (K <= 0) return CCE_ERR_INVALID_ARGUMENT;
+  if (M == 1) lda = int64_t(ceil_div(K, 16)) * 16;  // the stride of a single row says nothing
+  if (N == 1) ldb = int64_t(ceil_div(K, 16)) * 16;
+  s = check_codes(A, lda, SA, K);
+  if (s == CCE_OK) s = check_codes(B, ldb, SB, K);
+  if (s != CCE_OK) return s;
+  if (!aligned16(A) || !aligned16(B) || lda % 16 != 0 || ldb % 16 != 0 || ws == nullptr ||
+      !aligned16(ws))
+    return CCE_ERR_INVALID_ARGUMENT;
+  if (ws_bytes < kStatusBytes) return CCE_ERR_WORKSPACE_TOO_SMALL;
+  if (K > kMaxQuantD || ceil_div(M, 128) * ceil_div(N, 128) >= int64_t(1) << 31)
+    return CCE_ERR_UNSUPPORTED;
+  int sms = 0;
+  s = device_info(&sms);
+  if (s != CCE_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Fp8Args a;
+  std::memset(&a, 0, sizeof(a));
+  a.M = int(M);
+  a.N = int(N);
+  a.G = int(ceil_div(K, QGROUP));
+  a.sa = SA;
+  a.sb = SB;
+  a.c = C;
+  a.ldc = ldc;
+  a.c_bf16 = c_dtype == CCE_BF16;
+  a.vec = rows16(C, ldc, dtype_bytes(c_dtype));
+  a.wait_ns = g_wait_ns.load();
+  a.status = status_word(ws);
+  ProfScope ps(PK_FP8, st);
+  const int64_t np = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int64_t tiles = ceil_div(N, 128);
+  const int S = few_split(tiles, a.G, sms);
+  if (M <= 128 && np * ceil_div(a.G, S) <= FF_MAX_SCALES) {
+    a.n_ct = int(tiles);
+    switch (np) {
+      case 16: return launch_few<16>(A, lda, B, ldb, K, S, sms, a, st);
+      case 32: return launch_few<32>(A, lda, B, ldb, K, S, sms, a, st);
+      case 64: return launch_few<64>(A, lda, B, ldb, K, S, sms, a, st);
+      default: return launch_few<128>(A, lda, B, ldb, K, S, sms, a, st);
+    }
+  }
+  static bool done[64];
+  s = set_smem_once(fp8_rows_kernel, F8_SMEM, done);
+  if (s != CCE_OK) return s;
+  a.n_rt = int(ceil_div(M, F8_BM));
+  a.n_ct = int(ceil_div(N, F8_BN));
+  // row tiles of one raster group: 48 MB of A, so that a group stays in L2
+  // while the columns pass
+  a.group_rt = int(std::max<int64_t>(
+      1, std::min<int64_t>(a.n_rt, (int64_t(48) << 20) / (F8_BM * K))));
+  CUtensorMap ma, mb;
+  if (!make_fp8_map(&ma, A, M, K, lda, F8_BM) || !make_fp8_map(&mb, B, N, K, ldb, F8_BN))
+    return CCE_ERR_CUDA;
+  fp8_rows_kernel<<<grid_for(int64_t(a.n_rt) * a.n_ct, sms), F8_THREADS, F8_SMEM, st>>>(ma, mb, a);
   return launch_ok();
 }
 

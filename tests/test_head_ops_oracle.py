@@ -97,6 +97,23 @@ def test_norm_refusals(lib):
     assert lib.cce_norm_backward_workspace_bytes(4, 16385) == 0
 
 
+def test_matmul_refusals(lib):
+    ok = dict(A=P, lda=128, SA=P, B=P, ldb=128, SB=P, M=4, N=300, K=128, C=P, ct=1, ldc=300, ws=P,
+              n=256, stream=None)
+
+    def call(**kw):
+        return lib.cce_fp8_matmul(*{**ok, **kw}.values())
+
+    for kw in (dict(A=None), dict(SA=None), dict(B=None), dict(SB=None), dict(C=None),
+               dict(ws=None), dict(A=P + 8), dict(B=P + 8), dict(ws=P + 8), dict(C=P + 1),
+               dict(lda=136), dict(ldb=136), dict(lda=112), dict(ldc=299), dict(ct=2), dict(M=0),
+               dict(N=0), dict(K=0), dict(SA=P + 2)):
+        assert call(**kw) == 1, kw
+    assert call(n=255) == 4
+    assert call(K=65537, lda=65552, ldb=65552) == 2
+    assert call(M=1 << 30, N=1 << 30, ldc=1 << 30) == 2
+
+
 def test_binding_refuses_what_the_library_would_misread():
     cpu = torch.zeros(4, 128)
     with pytest.raises(ValueError, match="CUDA"):
