@@ -316,7 +316,7 @@ def _run_own(s):
         cce.cce_fp8_matmul(s["a"], s["sa"], s["b"], s["sb"], s["c"], s["ws"])
         return s["c"]
     cce.cce_sample_rows(s["logits"], s["t"], s["k"], s["p"], s["minp"], s["u"], s["tok"],
-                        s["logp"], s["ws"])
+                        s["logp"])
     return s["tok"], s["logp"]
 
 
