@@ -509,7 +509,7 @@ cce_status cce_forward_noalloc(const void* H, int64_t M, const cce_head* W,
 
 /* ==========================================================================
  * Operators around the head: 8-bit rows and weights and their product, the
- * final norm with an 8-bit checkpoint of its input.
+ * final norm with an 8-bit checkpoint of its input, and sampling.
  *
  * The conventions at the top of this file hold, with these additions:
  * - Matrices are row-major; ldX is the distance of two rows, in elements
@@ -595,6 +595,33 @@ cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs,
                              cce_dtype dh_dtype, int64_t lddh, void* dX,
                              cce_dtype dx_dtype, int64_t lddx, float* dW,
                              void* ws, size_t ws_bytes, cce_stream_t stream);
+
+/*
+ * One token for each row of logits [B, V], f32 or bf16, V <= 2^24, from a
+ * given uniform number.  With the live logits (neither -inf nor NaN) of a row
+ * ranked by value, equal ones by index, and w = exp((l - max) / temperature):
+ *   top_k:  the first k ranks stay              (k <= 0: all)
+ *   top_p:  of these, the shortest prefix whose mass is at least top_p of
+ *           theirs, one rank at least           (top_p >= 1: all)
+ *   min_p:  of these, those with w >= min_p     (min_p <= 0: all; the first
+ *           rank always stays)
+ *   token:  the first rank whose running mass exceeds u times the mass of
+ *           what stays, 0 <= u < 1 (numbers outside are moved inside)
+ * A temperature that is not above 0 takes the first rank.  Several +inf share
+ * the row.  A row without live logits gives token -1.
+ * temperature, top_p, min_p, u: fp32 [B]; top_k: int32 [B]; all but u may be
+ * NULL (1, all, all, all).  tokens: int32 [B].  logp: fp32 [B] or NULL, the
+ * token's log-softmax over all live logits at temperature 1, which is
+ * cce_forward's logp for that label (0 for token -1).
+ * Masses are sums of fixed-point numbers (weights in fp64, rounded to
+ * 2^-45, for V above 2^18 to 2^-(63 - ceil(log2 V))), so the tokens do not
+ * depend on the order of summation.  One kernel, no workspace.
+ */
+cce_status cce_sample_rows(const void* logits, cce_dtype dtype, int64_t B,
+                           int64_t V, int64_t ld, const float* temperature,
+                           const int32_t* top_k, const float* top_p,
+                           const float* min_p, const float* u, int32_t* tokens,
+                           float* logp, cce_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -141,6 +141,11 @@ _SIGS = {
                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                       ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "cce_sample_rows": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p]),
     "cce_norm_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                         ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                         ctypes.c_int, ctypes.c_double, ctypes.c_void_p,
@@ -709,3 +714,24 @@ def cce_norm_backward(X8, Xs, rstd, w, dH, dX, dW=None, ws=None, stream=None):
     _run("cce_norm_backward", dev, stream, x8, ldx8, xs, _dense("rstd", rstd, _F32, (M,), dev),
          M, D, _dense("w", w, _MAT_TYPES, (D,), dev), _MAT_TYPES[w.dtype], dh, dht, lddh, dx, dxt,
          lddx, None if dW is None else _dense("dW", dW, _F32, (D,), dev), p, n)
+
+
+_I32 = {torch.int32: 0}
+
+
+def cce_sample_rows(logits, temperature, top_k, top_p, min_p, u, tokens, logp=None, stream=None):
+    """One token for each row of ``logits`` [B, V] (f32 or bf16) from the
+    uniform numbers ``u`` [B]: ``temperature``, ``top_p``, ``min_p`` fp32 [B]
+    and ``top_k`` int32 [B], each of the four None for none.  ``tokens`` int32
+    [B] (-1 for a row that is masked throughout); ``logp`` fp32 [B], the
+    tokens' log-softmax at temperature 1."""
+    (B, V), dev = logits.shape, logits.get_device()
+    l, lt, ld = _mat("logits", logits, _MAT_TYPES, B, V, dev)
+    row = (B,)
+    _run("cce_sample_rows", dev, stream, l, lt, B, V, ld,
+         None if temperature is None else _dense("temperature", temperature, _F32, row, dev),
+         None if top_k is None else _dense("top_k", top_k, _I32, row, dev),
+         None if top_p is None else _dense("top_p", top_p, _F32, row, dev),
+         None if min_p is None else _dense("min_p", min_p, _F32, row, dev),
+         _dense("u", u, _F32, row, dev), _dense("tokens", tokens, _I32, row, dev),
+         None if logp is None else _dense("logp", logp, _F32, row, dev))

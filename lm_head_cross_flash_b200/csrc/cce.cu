@@ -99,7 +99,7 @@ bool make_map(CUtensorMap* m, const void* ptr, bool bf16, uint64_t cols,
 enum ProfKind {
   PK_SPLIT = 0, PK_LSE, PK_MERGE, PK_ORPO, PK_SKIP, PK_GRAD, PK_DH, PK_SELFTEST, PK_DHSUM,
   PK_PREFIX, PK_DW, PK_DEQ, PK_FUSED, PK_FSUM, PK_SLICE, PK_SSUM, PK_QFWD,
-  PK_QUANT, PK_NORM, PK_FP8, PK_N
+  PK_QUANT, PK_NORM, PK_FP8, PK_SAMPLE, PK_N
 };
 const char* const kProfNames[PK_N] = {"operand_prep",  "fwd_lse_gemm", "lse_merge",
                                       "orpo_epilogue", "skip_plan",    "bwd_grad_gemm",
@@ -108,7 +108,8 @@ const char* const kProfNames[PK_N] = {"operand_prep",  "fwd_lse_gemm", "lse_merg
                                       "dequant_chunk", "bwd_fused",
                                       "fused_part_sum", "bwd_sliced",
                                       "sliced_part_sum", "fwd_q_small_m",
-                                      "fp8_quant", "final_norm", "fp8_matmul"};
+                                      "fp8_quant", "final_norm", "fp8_matmul",
+                                      "sample_rows"};
 struct ProfRec {
   int kind;
   cudaEvent_t a, b;

@@ -5,6 +5,7 @@
 
 #include "fp8_mm.cuh"
 #include "row_ops.cuh"
+#include "sample.cuh"
 
 namespace {
 
@@ -142,6 +143,45 @@ cce_status launch_few(const void* A, int64_t lda, const void* B, int64_t ldb, in
   cfg.attrs = at;
   cfg.numAttrs = S > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, fp8_few_kernel<NP>, ma, mb, args, S) == cudaSuccess
+             ? launch_ok()
+             : (cudaGetLastError(), CCE_ERR_CUDA);
+}
+
+// CTAs (a power of two up to 8) that share a row of logits: enough that the
+// row's slices stay in shared memory with two CTAs on an SM, and more for a
+// few rows, down to 8,192 logits a CTA.
+constexpr int kSampleTwoPerSm = 80 * 1024;
+constexpr int kSampleMaxSlice = 190 * 1024;
+int sample_cluster(int64_t B, int64_t V, int64_t bytes, int sms) {
+  int c = 1;
+  while (c < SA_MAX_CLUSTER && (ceil_div(V, c) * bytes > kSampleTwoPerSm ||
+                                (2 * c * B <= sms && V > 8192 * c)))
+    c *= 2;
+  return c;
+}
+
+template <typename T>
+cce_status launch_sample(SampleArgs a, int64_t B, cudaStream_t st) {
+  static bool done[64];
+  cce_status s = set_smem_once(sample_kernel<T>, kSampleMaxSlice, done);
+  if (s != CCE_OK) return s;
+  const int c = sample_cluster(B, a.V, sizeof(T), sm_count_guess());
+  a.slice = int(ceil_div(ceil_div(a.V, c), 8)) * 8;
+  const int64_t bytes = int64_t(a.slice) * sizeof(T);
+  a.resident = bytes <= kSampleMaxSlice;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(B) * c);
+  cfg.blockDim = dim3(SA_THREADS);
+  cfg.dynamicSmemBytes = a.resident ? size_t(bytes) : 0;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(c);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a) == cudaSuccess
              ? launch_ok()
              : (cudaGetLastError(), CCE_ERR_CUDA);
 }
@@ -363,6 +403,41 @@ cce_status cce_fp8_matmul(const uint8_t* A, int64_t lda, const float* SA, const 
     return CCE_ERR_CUDA;
   fp8_rows_kernel<<<grid_for(int64_t(a.n_rt) * a.n_ct, sms), F8_THREADS, F8_SMEM, st>>>(ma, mb, a);
   return launch_ok();
+}
+
+cce_status cce_sample_rows(const void* logits, cce_dtype dtype, int64_t B, int64_t V, int64_t ld,
+                           const float* temperature, const int32_t* top_k, const float* top_p,
+                           const float* min_p, const float* u, int32_t* tokens, float* logp,
+                           cce_stream_t stream) {
+  const cce_status s = check_matrix(logits, dtype, B, V, ld);
+  if (s != CCE_OK) return s;
+  if (u == nullptr || tokens == nullptr) return CCE_ERR_INVALID_ARGUMENT;
+  for (const void* p : {static_cast<const void*>(temperature), static_cast<const void*>(top_k),
+                        static_cast<const void*>(top_p), static_cast<const void*>(min_p),
+                        static_cast<const void*>(u), static_cast<const void*>(tokens),
+                        static_cast<const void*>(logp)})
+    if (!aligned_to(p, 4)) return CCE_ERR_INVALID_ARGUMENT;
+  if (V > (int64_t(1) << 24) || B > (int64_t(1) << 24)) return CCE_ERR_UNSUPPORTED;
+  SampleArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.logits = logits;
+  a.ld = ld;
+  a.V = int(V);
+  a.vec = rows16(logits, ld, dtype_bytes(dtype));
+  int log2v = 0;
+  while ((int64_t(1) << log2v) < V) ++log2v;
+  a.bits = std::min(45, 63 - log2v);  // a row's mass stays below 2^63
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u;
+  a.token = tokens;
+  a.logp = logp;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  ProfScope ps(PK_SAMPLE, st);
+  return dtype == CCE_F32 ? launch_sample<float>(a, B, st)
+                          : launch_sample<__nv_bfloat16>(a, B, st);
 }
 
 }  // extern "C"

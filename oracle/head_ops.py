@@ -85,3 +85,35 @@ def norm_backward(n, rstd, w, dh):
     g = dh * np.asarray(w, np.float64)
     dx = rstd[:, None] * (g - n * (g * n).mean(1, keepdims=True))
     return dx, (dh * n).sum(0)
+
+
+def sample_row(logits, temperature, top_k, top_p, min_p, u):
+    """(token, logp, ranked ids that stay) of one row; (-1, 0.0, []) for a row
+    without live logits."""
+    l = np.asarray(logits, np.float64)
+    ids = np.flatnonzero(l > -np.inf)
+    if ids.size == 0:
+        return -1, 0.0, ids
+    l = l[ids]
+    top = l.max()
+    with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+        d = np.where(l == top, 0.0, l - top)
+        order = np.argsort(-l, kind="stable")
+        n = order.size
+        if not temperature > 0:
+            n, w = 1, np.ones(1)
+        else:
+            e = np.where(d[order] == 0, 0.0, d[order] / np.float64(temperature))
+            w = np.exp(e)
+            if top_k > 0:
+                n = min(n, int(top_k))
+            if top_p < 1:
+                c = np.cumsum(w[:n])
+                n = min(n, max(1, int((c < float(top_p) * c[-1]).sum()) + 1))
+            if min_p > 0:
+                n = min(n, max(1, int((w[:n] >= min(float(min_p), 1.0)).sum())))
+        c = np.cumsum(w[:n])
+        u = min(max(float(u), 0.0), 1.0 - 2.0 ** -24)
+        at = order[min(n - 1, int((c <= u * c[-1]).sum()))]
+        logp = d[at] - np.log1p(np.exp(np.delete(d, int(np.argmax(l)))).sum())
+    return int(ids[at]), float(logp), ids[order[:n]]

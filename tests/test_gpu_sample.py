@@ -1,0 +1,242 @@
+"""Row sampling on the GPU against the float64 oracle.
+
+Tokens are compared for equality: the running masses of the two differ by a
+few 2^-45 of the largest weight a token, so a number u chosen without regard
+to the row decides otherwise with a probability below 1e-8 a row.  logp: the
+sum of the other weights is made of fp32 exponentials, each off by 2^-22 and
+by its argument's rounding (at most 104 * 2^-24 where it does not vanish), so
+|error| <= 7e-6 min(1, sum) plus the output's half step, 2^-24 relative.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from lm_head_cross_flash_b200 import cce
+from oracle import head_ops as O
+
+pytestmark = pytest.mark.gpu
+
+
+def t32(x, dtype=torch.float32):
+    return torch.tensor(np.asarray(x), dtype=dtype, device="cuda")
+
+
+def run(l, t=None, k=None, p=None, mp=None, u=None, with_logp=True, stream=None):
+    B = l.shape[0]
+    tok = torch.full((B,), -7, dtype=torch.int32, device="cuda")
+    lp = torch.full((B,), float("nan"), device="cuda") if with_logp else None
+    cce.cce_sample_rows(l, None if t is None else t32(t), None if k is None else t32(k, torch.int32),
+                        None if p is None else t32(p), None if mp is None else t32(mp),
+                        t32(u), tok, lp, stream)
+    torch.cuda.synchronize()
+    return tok.cpu().numpy(), None if lp is None else lp.cpu().numpy()
+
+
+def check(l, t=None, k=None, p=None, mp=None, u=None):
+    B = l.shape[0]
+    tok, lp = run(l, t, k, p, mp, u)
+    x = l.float().cpu().numpy().astype(np.float64)
+    f = lambda v, d: np.full(B, d) if v is None else np.asarray(v)
+    t, k, p, mp = f(t, 1.0), f(k, 0), f(p, 1.0), f(mp, 0.0)
+    u = np.asarray(u)
+    for r in range(B):
+        g = lambda v: float(np.float32(v[r]))
+        want, wlp, _ = O.sample_row(x[r], g(t), int(k[r]), g(p), g(mp), g(u))
+        what = (r, g(t), int(k[r]), g(p), g(mp), g(u))
+        assert tok[r] == want, (what, tok[r], want)
+        rest = 0.0 if want < 0 else np.expm1(-min(wlp, 0.0)) if tok[r] == np.nanargmax(x[r]) else 1.0
+        assert abs(lp[r] - wlp) <= 7e-6 * min(1.0, rest) + 2.0 ** -24 * abs(wlp) + 1e-30, (what, lp[r], wlp)
+    return tok
+
+
+def logits(seed, B, V, dtype, spread=2.5, peaks=True, masked=0.0, pad=0):
+    r = np.random.default_rng(seed)
+    x = spread * r.standard_normal((B, V + pad))
+    if peaks:
+        for b in range(B):
+            n = min(V, 40)
+            x[b, r.integers(0, V, n)] = spread * (4 + 1.5 * r.uniform(0.2, 1.2) * r.exponential(size=n))
+    if masked:
+        x[r.random(x.shape) < masked] = -np.inf
+    return t32(x).to(dtype)[:, :V]
+
+
+def settings(seed, B):
+    r = np.random.default_rng(seed)
+    return dict(t=r.choice([0.0, 0.3, 0.7, 1.0, 1.0, 1.5, 3.0], B),
+                k=r.choice([0, 0, 1, 2, 20, 50, 500, 3000, 10 ** 6], B),
+                p=r.choice([1.0, 1.0, 0.0, 0.1, 0.5, 0.9, 0.95, 0.999], B),
+                mp=r.choice([0.0, 0.0, 0.01, 0.1, 0.5, 1.0], B), u=r.random(B).astype(np.float32))
+
+
+BF, F = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 63, 1000, 4097, 8192])
+@pytest.mark.parametrize("masked", [0.0, 0.5, 0.99])
+def test_small_vocabularies(V, dtype, masked):
+    B = 40
+    check(logits(V, B, V, dtype, masked=masked), **settings(V + 1, B))
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("B,V,spread,peaks", [(1, 73440, 2.5, True), (3, 128256, 1.0, False),
+                                              (24, 50001, 4.0, True), (10, 262144, 1.0, False),
+                                              (40, 32000, 0.1, False), (160, 20000, 2.5, True)])
+def test_large_vocabularies(B, V, spread, peaks, dtype):
+    l = logits(V, B, V, dtype, spread, peaks, pad=3)
+    for seed in range(3 if B < 100 else 1):
+        check(l, **settings(seed, B))
+    n = np.random.default_rng(9).random(B).astype(np.float32)
+    check(l, u=n)                       # plain
+    check(l, p=[0.95] * B, u=n)         # nucleus alone
+    check(l, mp=[0.02] * B, t=[1.3] * B, u=n)
+    check(l, k=[50] * B, u=n)
+    check(l, k=[V // 2] * B, p=[0.9] * B, u=n)
+
+
+def test_rows_without_and_with_one_live_logit():
+    l = torch.full((6, 5000), float("-inf"), device="cuda")
+    l[1, 4999] = -1e30
+    l[2, 17] = float("nan")
+    l[3] = float("nan")
+    l[4, 3], l[4, 4] = 5.0, float("nan")
+    l[5, 0] = torch.finfo(F).min
+    tok = check(l, t=[1.0] * 6, k=[0, 5, 0, 3, 0, 0], p=[0.9] * 6, mp=[0.1] * 6, u=[0.5] * 6)
+    assert tok.tolist() == [-1, 4999, -1, -1, 3, 0]
+
+
+def test_masks_of_the_lowest_value_stay_live():
+    """A mask of the type's lowest finite value is a logit like others: it is
+    chosen only where nothing else is."""
+    for dtype in (F, BF):
+        l = torch.full((3, 3000), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+        l[1, 100] = 0.0
+        l[2, 5:8] = 1.0
+        check(l, u=[0.5, 0.999, 0.9])
+        check(l, k=[1000] * 3, p=[0.9] * 3, t=[2.0] * 3, u=[0.5, 0.999, 0.9])
+
+
+def test_infinities_share_the_row():
+    l = logits(5, 5, 2000, F)
+    l[0, 7] = float("inf")
+    l[1, [3, 900, 1999]] = float("inf")
+    l[2] = float("inf")
+    l[3, 1] = float("-inf")
+    l[4, [2, 1000]] = float("inf")
+    check(l, u=[0.4, 0.7, 0.123, 0.5, 0.9])
+    check(l, k=[100] * 5, p=[0.6] * 5, mp=[0.5] * 5, t=[0.5] * 5, u=[0.4, 0.7, 0.123, 0.5, 0.9])
+
+
+@pytest.mark.parametrize("V", [5, 2048, 2049, 40000, 300001])
+def test_equal_logits(V):
+    """One value, two values, and signed zeros: ranks go by index."""
+    l = torch.zeros(4, V, device="cuda")
+    l[1, ::2] = -0.0
+    l[2, ::3] = 1.0
+    l[3] = -3.25
+    for u in (0.0, 0.25, 0.77, 0.9999):
+        check(l, u=[u] * 4)
+        check(l, k=[V // 2 + 1] * 4, u=[u] * 4)
+        check(l, p=[0.5] * 4, u=[u] * 4)
+        check(l, mp=[1.0] * 4, k=[0, 3, 0, V // 3 + 1], u=[u] * 4)
+
+
+def test_few_values_many_ties():
+    r = np.random.default_rng(3)
+    l = t32(r.integers(0, 6, (6, 60000)) * 0.5)
+    for s in range(3):
+        check(l, **settings(s + 20, 6))
+
+
+def test_extreme_ranges_and_temperatures():
+    r = np.random.default_rng(4)
+    x = r.standard_normal((8, 30000)) * np.array([1e-30, 1e-6, 1, 1e3, 1e10, 1e30, 3e37, 1e-3])[:, None]
+    l = t32(x)
+    for t in (1e-30, 1e-6, 0.05, 1.0, 50.0, 1e10, 3e38, float("inf")):
+        check(l, t=[t] * 8, u=r.random(8).astype(np.float32))
+        check(l, t=[t] * 8, k=[4000] * 8, p=[0.7] * 8, u=r.random(8).astype(np.float32))
+        check(l, t=[t] * 8, mp=[0.3] * 8, u=r.random(8).astype(np.float32))
+
+
+def test_long_tails_beyond_the_weights_range():
+    """Mass far below the smallest weight, and targets next to the total."""
+    V = 100000
+    l = torch.linspace(0, -500, V, device="cuda").repeat(5, 1)
+    l[1, 1:] -= 60.0
+    l[2, 1:] -= 25.0
+    l[3, V // 2:] = -1e30
+    l[4] = l[4].flip(0)
+    for u in (0.0, 0.5, 1.0 - 2.0 ** -24):
+        for p in (1.0, 0.9999, 1.0 - 2.0 ** -24):
+            check(l, p=[p] * 5, u=[u] * 5)
+            check(l, p=[p] * 5, k=[60000] * 5, u=[u] * 5)
+
+
+def test_numbers_outside_their_ranges():
+    l = logits(6, 8, 3000, F)
+    nan = float("nan")
+    tok, _ = run(l, u=[-1.0, nan, 0.0, 1.0, 2.0, 1.0 - 2.0 ** -24, 0.5, 0.5],
+                 t=[1, 1, 1, 1, 1, 1, nan, -2.0])
+    a, _ = run(l, u=[0.0] * 3 + [1.0 - 2.0 ** -24] * 3 + [0.5] * 2, t=[1.0] * 6 + [0.0] * 2)
+    assert (tok == a).all()
+    check(l, u=[0.3] * 8, p=[-1.0, 0.0, 5.0, 1.0, 0.5, 0.5, 0.5, 0.5], k=[-3, 0, 2 ** 31 - 1] + [4] * 5,
+          mp=[-1.0, 0.0, 2.0, 1.0] + [0.1] * 4)
+    b, _ = run(l, u=[0.3] * 8, p=[nan] * 8, mp=[nan] * 8)
+    c, _ = run(l, u=[0.3] * 8)
+    assert (b == c).all()
+
+
+def test_a_vocabulary_beyond_shared_memory():
+    """V = 1,000,003: the slices are read from memory in every pass."""
+    l = logits(7, 2, 1000003, F, 1.0, False)
+    check(l, u=[0.2, 0.9])
+    check(l, k=[40, 700000], p=[0.9, 0.99], u=[0.2, 0.9])
+
+
+def test_the_draw_follows_the_probabilities():
+    """Each token's share of evenly spaced numbers is its probability to
+    within one spacing."""
+    V, n = 50, 1000
+    l = logits(8, 1, V, F, 1.0, False)
+    tok, _ = run(l.expand(n, V).contiguous(), u=(np.arange(n) + 0.5) / n, with_logp=False)
+    p = torch.softmax(l[0].double(), 0).cpu().numpy()
+    assert (np.abs(np.bincount(tok, minlength=V) / n - p) <= 1.0 / n + 1e-12).all()
+
+
+def test_repeats_on_a_stream_and_in_a_graph():
+    l, s = logits(9, 33, 60000, BF), settings(30, 33)
+    tok, lp = run(l, **s)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    tok2, lp2 = run(l, **s, stream=side)
+    assert (tok == tok2).all() and (lp == lp2).all()
+    a = {k: t32(v, torch.int32 if k == "k" else F) for k, v in s.items()}
+    out, lps = torch.zeros(33, dtype=torch.int32, device="cuda"), torch.zeros(33, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cce.cce_sample_rows(l, a["t"], a["k"], a["p"], a["mp"], a["u"], out, lps)
+    g.replay()
+    torch.cuda.synchronize()
+    assert (out.cpu().numpy() == tok).all() and (lps.cpu().numpy() == lp).all()
+    a["u"].uniform_()
+    g.replay()
+    check(l, **{**s, "u": a["u"].cpu().numpy()})
+
+
+def test_logp_is_the_forward_pass_s():
+    """The token's logp is cce_forward's for that label."""
+    M, D, V = 20, 256, 3000
+    g = torch.Generator(device="cuda").manual_seed(3)
+    H = torch.randn(M, D, generator=g, device="cuda")
+    W = torch.randn(V, D, generator=g, device="cuda") * 0.2
+    l = (H.double() @ W.double().T).float()
+    tok, lp = run(l, u=np.random.default_rng(1).random(M).astype(np.float32))
+    head = cce.Head(w=W, V=V, D=D)
+    ws = cce.alloc_workspace(M, cce.CCE_F32, head)
+    logp, lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    cce.cce_forward(H, head, torch.from_numpy(tok).cuda(), logp, lse, ws=ws)
+    torch.cuda.synchronize()
+    assert np.abs(logp.cpu().numpy() - lp).max() <= 2e-3  # the head's own tolerance

@@ -114,6 +114,32 @@ def test_matmul_refusals(lib):
     assert call(M=1 << 30, N=1 << 30, ldc=1 << 30) == 2
 
 
+def test_sampling_oracle_against_closed_forms():
+    l = np.log([0.5, 0.2, 0.1, 0.2])
+    s = lambda u, k=0, p=1.0, mp=0.0, t=1.0: O.sample_row(l, t, k, p, mp, u)
+    assert [s(u)[0] for u in (0.0, 0.49, 0.51, 0.69, 0.71, 0.89, 0.91)] == [0, 0, 1, 1, 3, 3, 2]
+    assert abs(s(0.6)[1] - np.log(0.2)) < 1e-12
+    assert s(0.99, k=2)[0] == 1 and s(0.99, p=0.6)[0] == 1 and s(0.99, mp=0.45)[0] == 0
+    assert s(0.99, k=3, p=0.75)[2].tolist() == [0, 1]   # 0.7 of 0.9 is enough
+    assert s(0.7, t=0.0)[0] == 0 and s(0.99, p=0.0)[0] == 0 and s(0.99, mp=5.0)[0] == 0
+    assert O.sample_row([-np.inf, np.nan], 1, 0, 1, 0, 0.5)[:2] == (-1, 0.0)
+    assert O.sample_row([1.0, np.inf, np.inf], 1, 0, 1, 0, 0.6)[0] == 2
+
+
+def test_sample_refusals(lib):
+    ok = dict(l=P, dt=1, B=4, V=100, ld=100, t=P, k=P, p=P, mp=P, u=P, tok=P, logp=P, stream=None)
+
+    def call(**kw):
+        return lib.cce_sample_rows(*{**ok, **kw}.values())
+
+    for kw in (dict(l=None), dict(u=None), dict(tok=None), dict(B=0), dict(V=0), dict(ld=99),
+               dict(dt=3), dict(l=P + 1), dict(t=P + 1), dict(k=P + 2), dict(p=P + 1),
+               dict(mp=P + 1), dict(u=P + 1), dict(tok=P + 2), dict(logp=P + 1)):
+        assert call(**kw) == 1, kw
+    assert call(V=(1 << 24) + 1, ld=1 << 25) == 2
+    assert call(B=(1 << 24) + 1) == 2
+
+
 def test_binding_refuses_what_the_library_would_misread():
     cpu = torch.zeros(4, 128)
     with pytest.raises(ValueError, match="CUDA"):
