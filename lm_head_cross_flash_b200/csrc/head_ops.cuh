@@ -147,32 +147,25 @@ cce_status launch_few(const void* A, int64_t lda, const void* B, int64_t ldb, in
              : (cudaGetLastError(), CCE_ERR_CUDA);
 }
 
-// CTAs (a power of two up to 8) that share a row of logits: enough that the
-// row's slices stay in shared memory with two CTAs on an SM, and more for a
-// few rows, down to 8,192 logits a CTA.
-constexpr int kSampleTwoPerSm = 80 * 1024;
-constexpr int kSampleMaxSlice = 190 * 1024;
-int sample_cluster(int64_t B, int64_t V, int64_t bytes, int sms) {
+// CTAs (a power of two up to 8) that share a row of logits: as many as run at
+// once (two on an SM), down to 8,192 logits a CTA; and at most 2^21 logits.
+int sample_cluster(int64_t B, int64_t V, int sms) {
   int c = 1;
-  while (c < SA_MAX_CLUSTER && (ceil_div(V, c) * bytes > kSampleTwoPerSm ||
-                                (2 * c * B <= sms && V > 8192 * c)))
-    c *= 2;
+  while (c < SA_MAX_CLUSTER && ((c * B <= sms && V > 8192 * c) || V > int64_t(c) << 21)) c *= 2;
   return c;
 }
 
-template <typename T>
-cce_status launch_sample(SampleArgs a, int64_t B, cudaStream_t st) {
+template <typename T, int MODE>
+cce_status launch_sample(SampleArgs a, int64_t B, int c, cudaStream_t st) {
   static bool done[64];
-  cce_status s = set_smem_once(sample_kernel<T>, kSampleMaxSlice, done);
+  const cce_status s = set_smem_once(sample_kernel<T, MODE>, int(sizeof(SaShared)), done);
   if (s != CCE_OK) return s;
-  const int c = sample_cluster(B, a.V, sizeof(T), sm_count_guess());
-  a.slice = int(ceil_div(ceil_div(a.V, c), 8)) * 8;
-  const int64_t bytes = int64_t(a.slice) * sizeof(T);
-  a.resident = bytes <= kSampleMaxSlice;
+  a.slice = int(ceil_div(ceil_div(a.V, c), SA_SEG)) * SA_SEG;
+  a.seg_mul = int(ceil_div(a.slice / SA_SEG, SA_MAX_SEGS));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(B) * c);
   cfg.blockDim = dim3(SA_THREADS);
-  cfg.dynamicSmemBytes = a.resident ? size_t(bytes) : 0;
+  cfg.dynamicSmemBytes = sizeof(SaShared);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -181,9 +174,19 @@ cce_status launch_sample(SampleArgs a, int64_t B, cudaStream_t st) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<T>, a) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, sample_kernel<T, MODE>, a) == cudaSuccess
              ? launch_ok()
              : (cudaGetLastError(), CCE_ERR_CUDA);
+}
+
+// One launch where every row gets as many CTAs as it can use, else two.
+template <typename T>
+cce_status launch_sample_rows(const SampleArgs& a, int64_t B, cudaStream_t st) {
+  const int c = sample_cluster(B, a.V, sm_count_guess());
+  const int most = sample_cluster(1, a.V, sm_count_guess());
+  if (c == most) return launch_sample<T, SA_BOTH>(a, B, c, st);
+  const cce_status s = launch_sample<T, SA_LIST_ONLY>(a, B, c, st);
+  return s != CCE_OK ? s : launch_sample<T, SA_SEARCH_ONLY>(a, B, most, st);
 }
 
 }  // namespace
@@ -436,8 +439,8 @@ cce_status cce_sample_rows(const void* logits, cce_dtype dtype, int64_t B, int64
   a.logp = logp;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(PK_SAMPLE, st);
-  return dtype == CCE_F32 ? launch_sample<float>(a, B, st)
-                          : launch_sample<__nv_bfloat16>(a, B, st);
+  return dtype == CCE_F32 ? launch_sample_rows<float>(a, B, st)
+                          : launch_sample_rows<__nv_bfloat16>(a, B, st);
 }
 
 }  // extern "C"

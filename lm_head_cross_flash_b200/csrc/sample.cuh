@@ -13,16 +13,26 @@
 // in fp64 (Tang's table method: 2^(j/32) times a polynomial on |r| <= 1/64),
 // since a draw among 2^18 tokens is decided by differences far below fp32.
 //
-// Search.  A cluster of CTAs holds the row in shared memory, so the logits are
-// read from memory once.  One pass counts the live logits in 2,048 bins of
-// equal width below the maximum.  The counts, with the largest and smallest
-// weight that a bin can hold, bracket the bin in which the target is reached;
-// the few candidates of the bracket are collected, sorted by the cluster's
-// first CTA, and summed exactly.  A bracket that holds more candidates than
-// the list takes (a flat row, or many equal logits) is searched again with
-// 2,048 bins of its own, over its values or, where those are all equal, over
-// its indices, until it fits; a step that does not halve it is followed by a
-// bisection, so the search ends for every input.
+// Two ways.  A cluster of CTAs takes a row.  One pass over memory gives the
+// maximum, sums of fp32 exponentials (behind logp, and the total mass to a
+// known error) and the largest logit of every segment of 256.
+//  * List.  Nearly always the kept ranks are few.  The segments' maxima say
+//    below which value enough ranks, or enough mass, must lie; only segments
+//    that reach it are read again, and the candidates are sorted by the
+//    cluster's first CTA and summed exactly.  The result stands if the
+//    total's error leaves no doubt about it.
+//  * Search.  Otherwise (a flat row, many equal logits, a doubt) one pass
+//    counts the live logits in 2,048 bins of equal width below the maximum and
+//    sums their weights by bin, exactly (three 32-bit digits of 15 bits each
+//    by shared-memory atomics: 0.16 cycles a logit and SM for one or two of
+//    them, 0.7 to 2 for one 64-bit atomic).  The bin in which the target is
+//    reached is collected and sorted; one that holds more logits than the
+//    list takes is binned again, over its values or, where those are all
+//    equal, over its indices.  A step that does not halve it is followed by a
+//    bisection, so the search ends for every input.
+// Many rows run as two launches: the list with few CTAs a row (its fixed
+// costs, mostly waits, are paid by fewer CTAs), and the search with eight for
+// the rows that are left, so that one flat row does not hold up the batch.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -36,16 +46,29 @@ constexpr int SA_WARPS = SA_THREADS / 32;
 constexpr int SA_BINS = 2048;
 constexpr int SA_CAP = 2048;  // candidates of one list
 constexpr int SA_MAX_CLUSTER = 8;
+constexpr int SA_SEG = 256;        // logits that a warp reads at once: one segment
+constexpr int SA_MAX_SEGS = 1024;  // segments (or groups of them) of one CTA
+constexpr int SA_OPEN = 256;       // segments that the list opens if their mass is not enough
+constexpr int SA_RING = 64 * 1024; // copies in flight during the first pass
+constexpr int SA_FLUSH = 65536;    // logits that 15-bit digits can be summed over in 32 bits
+constexpr int SA_UNDECIDED = -2;   // token of a row that the first launch leaves to the second
+enum : int { SA_BOTH = 0, SA_LIST_ONLY = 1, SA_SEARCH_ONLY = 2 };  // what a launch does
 static_assert(SA_CAP == 4 * SA_THREADS && SA_BINS == 4 * SA_THREADS, "four entries per thread");
+
+// Relative error of the pass's sums of exponentials: 2^-22 of ex2.approx, the
+// two roundings of its argument (at most 50 where it counts: 50 ln 2 2^-23),
+// fp32 sums of 8 terms, and a factor with the same errors for each time that a
+// larger maximum turns up.  Together below 8e-6.
+constexpr double SA_SUM_ERROR = 0x1p-16;
 
 struct SampleArgs {
   const void* logits;
   int64_t ld;
   int V;
-  int slice;     // logits per CTA, a multiple of 8
-  int resident;  // the slice is kept in shared memory
-  int vec;       // rows start on 16-byte boundaries
-  int bits;      // binary places of a weight
+  int slice;    // logits per CTA, a multiple of SA_SEG
+  int seg_mul;  // segments that share an entry of segs[]
+  int vec;      // rows start on 16-byte boundaries
+  int bits;     // binary places of a weight
   const float* temperature;  // the next four may be null: 1, off, off, off
   const int32_t* top_k;
   const float* top_p;
@@ -74,27 +97,42 @@ __device__ __forceinline__ int rank_index(u64 c) { return int(0xFFFFFFFFu - uint
 struct SaPart {
   u64 hi, lo;  // largest and smallest rank
   u64 mass;
-  double tail;  // sum of exp(l - max) without the maximum itself
-  float least;
-  int n;
+};
+// The same after the first pass: the largest rank and the sums of
+// exp(l - m) and exp((l - m) / T) over the logits below its value m.
+struct SaFirst {
+  u64 hi;
+  double tail, z;
+  float least;  // of the segments' maxima
+  int n;        // instances of m, which the sums leave out
 };
 
 struct SaShared {
-  uint32_t tot[SA_BINS];   // level-0 counts of the cluster
-  uint32_t hist[SA_BINS];  // this CTA's counts
   union {
-    u64 list[SA_CAP];
-    uint32_t tot2[SA_BINS];  // counts of a finer search
+    uint8_t ring[SA_RING];  // first pass: each thread's own copies
+    uint16_t opened[SA_RING / 2];  // list: segments to read again
+    struct {
+      uint32_t tot[SA_BINS];  // search: the cluster's counts and masses
+      u64 mass[SA_BINS];
+      uint32_t hist[SA_BINS];  // and this CTA's: counts, digits of the masses
+      uint32_t dig[3][SA_BINS];
+    };
   };
-  double pow2[32];  // 2^(j/32)
+  uint32_t open[SA_BINS];  // first CTA: counts of the segments' maxima
+  u64 list[SA_CAP];
+  uint32_t segs[SA_MAX_SEGS];  // value keys of the segments' largest logits, 0: none
+  double pow2[32];             // 2^(j/32)
   SaPart parts[2][SA_MAX_CLUSTER];
   SaPart warp_part[SA_WARPS];
-  u64 warp_sum[3][SA_WARPS];
-  u64 res_rank, res_cum;
-  int lo_bin, hi_bin, last_bin;
-  uint32_t n_above, n_in;
-  int n_list;
-  int counts[SA_MAX_CLUSTER];
+  SaFirst firsts[SA_MAX_CLUSTER];
+  SaFirst warp_first[SA_WARPS];
+  u64 warp_sum[2][SA_WARPS];
+  u64 res_rank, res_cum, end;
+  u64 base;      // the measure above the bin
+  uint32_t n_in; // logits in it
+  int bin;
+  int n_list, n_opened;
+  int done;  // the list gave the answer
 };
 
 template <typename T>
@@ -122,23 +160,22 @@ __device__ __forceinline__ void raw_values(const SaRaw<T>& r, float (&v)[8]) {
 template <typename T>
 class Sampler {
  public:
-  __device__ Sampler(const SampleArgs& a, SaShared& s, uint4* store)
-      : a_(a), s_(s), store_(store), cl_(cooperative_groups::this_cluster()) {
+  __device__ Sampler(const SampleArgs& a, SaShared& s)
+      : a_(a), s_(s), cl_(cooperative_groups::this_cluster()) {
     C_ = int(cl_.num_blocks());
     me_ = int(cl_.block_rank());
     row_ = int(blockIdx.x) / C_;
     g_ = static_cast<const T*>(a.logits) + int64_t(row_) * a.ld;
     s0_ = int(min(int64_t(a.V), int64_t(me_) * a.slice));
     s1_ = int(min(int64_t(a.V), int64_t(s0_) + a.slice));
-    if (threadIdx.x < 32) s_.pow2[threadIdx.x] = exp2(double(threadIdx.x) / 32.0);
   }
 
+  template <int MODE>
   __device__ void run();
 
  private:
   const SampleArgs& a_;
   SaShared& s_;
-  uint4* store_;
   cooperative_groups::cluster_group cl_;
   int C_, me_, row_, s0_, s1_;
   const T* g_;
@@ -146,6 +183,7 @@ class Sampler {
   float max_ = 0.f;
   double c_ = 0.0;    // log2(e) / T
   float bin_scale_ = 0.f;
+  bool level0_ = false;  // tot and mass hold the bins below the row's maximum
 
   // ------------------------------------------------------------- passes --
   __device__ SaRaw<T> fetch(int c) const {
@@ -172,21 +210,23 @@ class Sampler {
     }
     return r;
   }
-  // Calls f(values, first index) on every piece of eight logits of the slice.
+  // Calls f(values, first index) on every piece of eight logits in [from, to)
+  // (from: a multiple of 8 in the slice).
   template <typename F>
-  __device__ void pass(F f) const {
-    const int plane = a_.slice / 8;
-    for (int c = s0_ + int(threadIdx.x) * 8; c < s1_; c += SA_THREADS * 8) {
-      SaRaw<T> r;
-      if (a_.resident) {
+  __device__ void pass(int from, int to, F f) const {
+    constexpr int STEP = SA_THREADS * 8, UN = sizeof(T) == 4 ? 2 : 4;
+    for (int c0 = from + int(threadIdx.x) * 8; c0 < to; c0 += STEP * UN) {
+      SaRaw<T> r[UN];
 #pragma unroll
-        for (int i = 0; i < int(sizeof(T) / 2); ++i) r.v[i] = store_[i * plane + (c - s0_) / 8];
-      } else {
-        r = fetch(c);
+      for (int k = 0; k < UN; ++k)
+        if (c0 + k * STEP < to) r[k] = fetch(c0 + k * STEP);
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        if (c0 + k * STEP >= to) break;
+        float v[8];
+        raw_values<T>(r[k], v);
+        f(v, c0 + k * STEP);
       }
-      float v[8];
-      raw_values<T>(r, v);
-      f(v, c);
     }
   }
 
@@ -220,50 +260,28 @@ class Sampler {
   }
 
   // ------------------------------------------------- block and cluster --
-  __device__ static SaPart merge(const SaPart& x, const SaPart& y) {
-    SaPart r;
-    r.hi = max(x.hi, y.hi);
-    r.lo = min(x.lo, y.lo);
-    r.mass = x.mass + y.mass;
-    r.tail = x.tail + y.tail;
-    r.least = fminf(x.least, y.least);
-    r.n = x.n + y.n;
-    return r;
-  }
-  __device__ static SaPart nothing() {
-    SaPart p;
-    p.hi = 0;
-    p.lo = ~u64(0);
-    p.mass = 0;
-    p.tail = 0.0;
-    p.least = INFINITY;
-    p.n = 0;
+  __device__ static SaPart nothing() { return SaPart{0, ~u64(0), 0}; }
+  __device__ static SaPart merge_lanes(SaPart p, int o) {
+    p.hi = max(p.hi, __shfl_xor_sync(0xffffffffu, p.hi, o));
+    p.lo = min(p.lo, __shfl_xor_sync(0xffffffffu, p.lo, o));
+    p.mass += __shfl_xor_sync(0xffffffffu, p.mass, o);
     return p;
   }
-  // The threads' parts of all CTAs, merged in a fixed order; every thread of
-  // the cluster gets the result.  Also a barrier of the cluster.
+  // The threads' parts of all CTAs, merged; every thread of the cluster gets
+  // the result.  Also a barrier of the cluster.
   __device__ SaPart exchange(SaPart p) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      SaPart q;
-      q.hi = __shfl_xor_sync(0xffffffffu, p.hi, o);
-      q.lo = __shfl_xor_sync(0xffffffffu, p.lo, o);
-      q.mass = __shfl_xor_sync(0xffffffffu, p.mass, o);
-      q.tail = __shfl_xor_sync(0xffffffffu, p.tail, o);
-      q.least = __shfl_xor_sync(0xffffffffu, p.least, o);
-      q.n = __shfl_xor_sync(0xffffffffu, p.n, o);
-      p = merge(p, q);
-    }
-    if ((threadIdx.x & 31) == 0) s_.warp_part[threadIdx.x >> 5] = p;
+    const int lane = threadIdx.x & 31;
+    for (int o = 16; o > 0; o >>= 1) p = merge_lanes(p, o);
+    if (lane == 0) s_.warp_part[threadIdx.x >> 5] = p;
     __syncthreads();
-    if (int(threadIdx.x) < C_) {
-      p = s_.warp_part[0];
-      for (int i = 1; i < SA_WARPS; ++i) p = merge(p, s_.warp_part[i]);
-      *cl_.map_shared_rank(&s_.parts[turn_][me_], threadIdx.x) = p;
+    if (threadIdx.x < 32) {
+      p = s_.warp_part[lane & (SA_WARPS - 1)];
+      for (int o = SA_WARPS / 2; o > 0; o >>= 1) p = merge_lanes(p, o);
+      if (lane < C_) *cl_.map_shared_rank(&s_.parts[turn_][me_], lane) = p;
     }
     cl_.sync();
-    p = s_.parts[turn_][0];
-    for (int i = 1; i < C_; ++i) p = merge(p, s_.parts[turn_][i]);
+    p = s_.parts[turn_][lane & (C_ - 1)];
+    for (int o = C_ / 2; o > 0; o >>= 1) p = merge_lanes(p, o);
     turn_ ^= 1;
     return p;
   }
@@ -280,96 +298,110 @@ class Sampler {
     for (int i = 0; i < warp; ++i) x += sums[i];
     return x;
   }
-  __device__ void clear_hist() {
-    for (int i = threadIdx.x; i < SA_BINS; i += SA_THREADS) s_.hist[i] = 0;
-    __syncthreads();
-  }
-  // The CTAs' counts added into `tot` of every CTA; barriers on both sides.
-  __device__ void total_hist(uint32_t* tot) {
-    cl_.sync();
-    const int n = SA_BINS / C_;
-    for (int i = threadIdx.x; i < n; i += SA_THREADS) {
-      const int b = me_ * n + i;
+  // Counts (and, by_mass, weights) of the logits by bin, of the whole cluster:
+  // bin(value, index) < 0 leaves a logit out.  Barriers of the cluster on both
+  // sides.
+  template <typename F>
+  __device__ void bin_up(bool by_mass, F bin) {
+    auto clear = [&](bool counts) {
+      for (int i = threadIdx.x; i < SA_BINS; i += SA_THREADS) {
+        if (counts) s_.hist[i] = 0;
+        s_.dig[0][i] = s_.dig[1][i] = s_.dig[2][i] = 0;
+      }
+    };
+    auto digits = [&](int r, int b) -> u64 {
+      const uint32_t(*d)[SA_BINS] = cl_.map_shared_rank(s_.dig, r);
+      return u64(d[0][b]) + (u64(d[1][b]) << 15) + (u64(d[2][b]) << 30);
+    };
+    clear(true);
+    const int n = SA_BINS / C_, b0 = me_ * n;  // the bins that this CTA adds up
+    u64 sum[SA_BINS / SA_THREADS] = {};
+    const int end = s0_ + a_.slice;  // the same number of rounds in every CTA
+    for (int c0 = s0_; c0 < end; c0 += SA_FLUSH) {
+      __syncthreads();
+      pass(c0, min(s1_, c0 + SA_FLUSH), [&](const float (&v)[8], int c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (!(v[j] > -INFINITY)) continue;
+          const int b = bin(v[j], c + j);
+          if (b < 0) continue;
+          atomicAdd(&s_.hist[b], 1u);
+          if (!by_mass) continue;
+          const u64 w = weight(v[j]);
+          if (w == 0) continue;
+          atomicAdd(&s_.dig[0][b], uint32_t(w) & 0x7FFFu);
+          atomicAdd(&s_.dig[1][b], uint32_t(w >> 15) & 0x7FFFu);
+          atomicAdd(&s_.dig[2][b], uint32_t(w >> 30));
+        }
+      });
+      cl_.sync();
+      for (int k = 0, i = threadIdx.x; i < n; ++k, i += SA_THREADS) {
+        u64 x = 0;
+        for (int r = 0; r < C_; ++r) x += digits(r, b0 + i);
+#pragma unroll
+        for (int q = 0; q < SA_BINS / SA_THREADS; ++q)
+          if (q == k) sum[q] += x;
+      }
+      if (c0 + SA_FLUSH < end) {
+        cl_.sync();
+        clear(false);
+      }
+    }
+    for (int k = 0, i = threadIdx.x; i < n; ++k, i += SA_THREADS) {
       uint32_t x = 0;
-      for (int r = 0; r < C_; ++r) x += *cl_.map_shared_rank(&s_.hist[b], r);
-      for (int r = 0; r < C_; ++r) *cl_.map_shared_rank(&tot[b], r) = x;
+      u64 y = 0;
+      for (int r = 0; r < C_; ++r) x += *cl_.map_shared_rank(&s_.hist[b0 + i], r);
+#pragma unroll
+      for (int q = 0; q < SA_BINS / SA_THREADS; ++q)
+        if (q == k) y = sum[q];
+      for (int r = 0; r < C_; ++r) {
+        *cl_.map_shared_rank(&s_.tot[b0 + i], r) = x;
+        *cl_.map_shared_rank(&s_.mass[b0 + i], r) = y;
+      }
     }
     cl_.sync();
   }
 
-  // Bins [lo_bin, hi_bin] that hold the rank at which the target is reached,
-  // and the counts above and inside, from the bins' counts.  edge(b, up): the
-  // largest / smallest weight that bin b can hold (by mass only).
-  template <typename E>
-  __device__ void bracket(const uint32_t* tot, bool by_mass, u64 target, E edge) {
-    const int b0 = threadIdx.x * 4;
-    u64 n[4], up[4], dn[4], sn = 0, su = 0, sd = 0;
+  __device__ void bin_level0() {
+    bin_up(true, [&](float l, int) { return bin_of(l); });
+    level0_ = true;
+  }
+
+  // The bin in which the running count or mass reaches the target (the last
+  // one if none does): bin, base (above it), n_in.
+  __device__ void locate(bool by_mass, u64 target) {
+    u64 x[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const u64 k = tot[b0 + i];
-      n[i] = sn += k;
-      up[i] = su += by_mass && k ? k * edge(b0 + i, true) : k;
-      dn[i] = sd += by_mass && k ? k * edge(b0 + i, false) : k;
-    }
-    if (threadIdx.x == 0) {
-      s_.lo_bin = s_.hi_bin = s_.last_bin = -1;
-      s_.n_above = s_.n_in = 0;
+      const int b = threadIdx.x * 4 + i;
+      x[i] = sum += by_mass ? s_.mass[b] : s_.tot[b];
     }
     __syncthreads();
-    const u64 en = scan(sn, s_.warp_sum[0]) - sn;
-    const u64 eu = scan(su, s_.warp_sum[1]) - su;
-    const u64 ed = scan(sd, s_.warp_sum[2]) - sd;
+    const u64 before = scan(sum, s_.warp_sum[0]) - sum;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const u64 u0 = i ? up[i - 1] : 0, d0 = i ? dn[i - 1] : 0;
-      // exactly one bin reaches the target first, if any does
-      if (eu + up[i] >= target && eu + u0 < target) s_.lo_bin = b0 + i;
-      if (ed + dn[i] >= target && ed + d0 < target) s_.hi_bin = b0 + i;
-      if (up[i] > u0) atomicMax(&s_.last_bin, b0 + i);
-    }
-    __syncthreads();
-    // the last bin that can hold any of the measure bounds both
-    const int last = max(s_.last_bin, 0);
-    const int lo = s_.lo_bin < 0 ? last : s_.lo_bin, hi = s_.hi_bin < 0 ? last : s_.hi_bin;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (b0 + i == lo - 1) s_.n_above = uint32_t(en + n[i]);
-      if (b0 + i == hi) s_.n_in = uint32_t(en + n[i]);  // up to here, for now
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s_.n_in -= s_.n_above;
-      s_.lo_bin = lo;
-      s_.hi_bin = hi;
+      const int b = threadIdx.x * 4 + i;
+      const u64 prev = before + (i ? x[i - 1] : 0);
+      if ((before + x[i] >= target || b == SA_BINS - 1) && (prev < target || b == 0)) {
+        s_.bin = b;
+        s_.base = prev;
+        s_.n_in = s_.tot[b];
+      }
     }
     __syncthreads();
   }
 
-  // This CTA's candidates go to its list; the caller's pass appends them.
+  // Candidates go to the first CTA's list.
   __device__ void append(u64 r) {
-    const int i = atomicAdd(&s_.n_list, 1);
-    if (i < SA_CAP) s_.list[i] = r;
+    const int i = atomicAdd(cl_.map_shared_rank(&s_.n_list, 0), 1);
+    if (i < SA_CAP) cl_.map_shared_rank(s_.list, 0)[i] = r;
   }
-  // All lists into the first CTA's, sorted there from the highest rank down.
-  // Returns the number of candidates (first CTA only).  Begins with a barrier
-  // of the cluster.
-  __device__ int gather_sorted() {
-    cl_.sync();
-    if (me_ != 0) return 0;
-    if (int(threadIdx.x) < C_)
-      s_.counts[threadIdx.x] = min(*cl_.map_shared_rank(&s_.n_list, threadIdx.x), SA_CAP);
-    __syncthreads();
-    int n = s_.counts[0];
-    for (int r = 1; r < C_; ++r) {
-      const u64* from = cl_.map_shared_rank(s_.list, r);
-      const int k = min(s_.counts[r], SA_CAP - n);
-      for (int i = threadIdx.x; i < k; i += SA_THREADS) s_.list[n + i] = from[i];
-      n += k;
-    }
+  // First CTA: sorts the list from the highest rank down; its length.
+  __device__ int sort_list() {
+    const int n = min(s_.n_list, SA_CAP);
     int len = 2;
     while (len < n) len *= 2;
-    for (int i = n + threadIdx.x; i < len; i += SA_THREADS) s_.list[i] = 0;
+    for (int i = n + int(threadIdx.x); i < len; i += SA_THREADS) s_.list[i] = 0;
     __syncthreads();
     for (int k = 2; k <= len; k *= 2)
       for (int j = k / 2; j > 0; j /= 2) {
@@ -426,17 +458,7 @@ class Sampler {
     cl_.sync();
   }
 
-  // Bins of equal width below the value vt: a logit l falls into bin
-  // min(2047, (vt - l) scale), so bin b holds vt - l in [b, b + 1) / scale,
-  // give or take the two roundings (below 2^-22 relative).  The largest or
-  // smallest weight that it can hold; nothing is known of the last bin's end.
-  __device__ u64 edge(int b, bool up, float vt, float scale) const {
-    if (!up && b == SA_BINS - 1) return 0;
-    const double d = up ? double(b) / double(scale) * (1.0 - 0x1p-20)
-                        : double(b + 1) / double(scale) * (1.0 + 0x1p-20);
-    const double off = vt == max_ ? 0.0 : double(vt) - double(max_);
-    return weight_log2((off - d) * c_);
-  }
+  // Bins of equal width below the value vt, the last one open.
   __device__ static int bin_below(float vt, float l, float scale) {
     return l == vt ? 0 : int(fminf((vt - l) * scale, float(SA_BINS - 1)));
   }
@@ -445,74 +467,87 @@ class Sampler {
     return s < 1e30f ? s : 1e30f;
   }
 
+  __device__ SaFirst first_pass(bool want_tail, bool want_z, float cz);
+  struct Settings {
+    float temp, tp;
+    int k;
+    bool use_p, use_m;
+    double u, thr;  // min_p as a bound on l - max
+  };
+  __device__ bool above_min(float l, const Settings& o) const {
+    return (l == max_ ? 0.0 : double(l) - double(max_)) >= o.thr;
+  }
+  __device__ static u64 nucleus(float tp, double z) {  // ceil(tp z), one at least
+    return u64(fmax(1.0, ceil(double(tp) * z)));
+  }
+  // Both set res_rank to the chosen rank; by_list returns false if it cannot
+  // be sure of it.
+  __device__ bool by_list(const Settings& o, const SaFirst& f);
+  __device__ __noinline__ void by_search(const Settings& o);
   // The rank at which the running count (by_mass: mass) reaches the target
   // (at least 1, at most the total): res_rank, and by mass res_cum.
-  __device__ void find(bool by_mass, u64 target);
+  __device__ __noinline__ void find(bool by_mass, u64 target);
   // Mass of the logits for which keep(value, index) holds.
   template <typename F>
   __device__ u64 mass_of(F keep) {
     SaPart p = nothing();
-    pass([&](const float (&v)[8], int c) {
+    pass(s0_, s1_, [&](const float (&v)[8], int c) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (v[j] > -INFINITY && keep(v[j], c + j)) p.mass += weight(v[j]);
     });
     return exchange(p).mass;
   }
-  __device__ static u64 part_of(double f, u64 z) {  // floor(f z), f in [0, 1)
-    const double x = floor(f * double(z));
-    return u64(x);
+  __device__ static u64 part_of(double f, double z) {  // floor(f z), f in [0, 1)
+    return u64(floor(f * z));
   }
 };
 
 template <typename T>
 __device__ void Sampler<T>::find(bool by_mass, u64 target) {
-  u64 top = ~u64(0), bottom = 0, base = 0;  // the bracket's ranks; the measure above it
-  float vt = max_, scale = bin_scale_;      // its bins: by value,
+  u64 top = ~u64(0), bottom = 0, base = 0;  // the ranks searched; the measure above them
+  float vt = max_, scale = bin_scale_;      // their bins: by value,
   int shift = -1;                           // or by index (one value)
-  const uint32_t* tot = s_.tot;
+  bool fits = false;
+  if (!level0_) bin_level0();
   // Every step leaves at most half of the ranks, so 64 steps are enough.
   for (int step = 0; step < 64; ++step) {
     const u64 top0 = top, bottom0 = bottom;
-    auto bin = [&](u64 r, float l) {
+    auto bin = [&](float l, int i) {
+      const u64 r = rank_of(l, i);
+      if (r > top0 || r < bottom0) return -1;
       return shift >= 0 ? int((top0 - r) >> shift) : bin_below(vt, l, scale);
     };
-    bracket(tot, by_mass, target - base, [&](int b, bool up) -> u64 {
-      return shift >= 0 ? weight(vt) : edge(b, up, vt, scale);
-    });
-    const bool whole = base == 0 && s_.n_above + s_.n_in <= SA_CAP;  // no pass for the mass above
-    const int lo = whole ? 0 : s_.lo_bin, hi = s_.hi_bin;
-    const uint32_t n_above = whole ? 0 : s_.n_above;
-    const bool fits = whole || s_.n_in <= SA_CAP;
-    __syncthreads();
+    if (step > 0)  // the first bins are there already
+      bin_up(by_mass, bin);
+    locate(by_mass, target - base);
+    base += s_.base;
+    fits = s_.n_in <= SA_CAP;
+    const int here = s_.bin;
     if (threadIdx.x == 0) s_.n_list = 0;
-    cl_.sync();  // the list's memory has been read
+    cl_.sync();
     SaPart p = nothing();
-    pass([&](const float (&v)[8], int c) {
+    pass(s0_, s1_, [&](const float (&v)[8], int c) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (!(v[j] > -INFINITY)) continue;
+        if (!(v[j] > -INFINITY) || bin(v[j], c + j) != here) continue;
         const u64 r = rank_of(v[j], c + j);
-        if (r > top0 || r < bottom0) continue;
-        const int b = bin(r, v[j]);
-        if (b < lo) {
-          if (by_mass) p.mass += weight(v[j]);
-        } else if (b <= hi) {
+        if (fits) {
+          append(r);
+        } else {
           p.hi = max(p.hi, r);
           p.lo = min(p.lo, r);
-          if (fits) append(r);
         }
       }
     });
+    if (fits) break;
     p = exchange(p);
-    base += by_mass ? p.mass : n_above;
-    if (fits || p.hi == 0) break;
     top = p.hi;
     bottom = p.lo;
     if (top - bottom > (top0 - bottom0) / 2) {
       const u64 mid = bottom + (top - bottom) / 2;
       p = nothing();
-      pass([&](const float (&v)[8], int c) {
+      pass(s0_, s1_, [&](const float (&v)[8], int c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (!(v[j] > -INFINITY)) continue;
@@ -535,22 +570,11 @@ __device__ void Sampler<T>::find(bool by_mass, u64 target) {
     } else {
       shift = max(0, 64 - __clzll((top - bottom) | 1) - 11);
     }
-    const u64 top1 = top, bottom1 = bottom;
-    clear_hist();
-    pass([&](const float (&v)[8], int c) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (!(v[j] > -INFINITY)) continue;
-        const u64 r = rank_of(v[j], c + j);
-        if (r <= top1 && r >= bottom1)
-          atomicAdd(&s_.hist[shift >= 0 ? int((top1 - r) >> shift) : bin_below(vt, v[j], scale)], 1u);
-      }
-    });
-    total_hist(s_.tot2);
-    tot = s_.tot2;
+    level0_ = false;
   }
-  const int n = gather_sorted();
+  cl_.sync();
   if (me_ == 0) {
+    const int n = sort_list();
     if (by_mass) {
       u64 r[4], cum[4];
       const u64 before = running_mass(n, base, r, cum);
@@ -562,194 +586,384 @@ __device__ void Sampler<T>::find(bool by_mass, u64 target) {
   share_result();
 }
 
+// The logits come in once.  Every warp keeps its own running maximum, so the
+// sums are relative to that until the end.
 template <typename T>
-__device__ void Sampler<T>::run() {
-  const int plane = a_.slice / 8;
-  // Pass 1: the logits come in (and stay, if they fit); maximum, least live
-  // value, number of live ones.
-  float m = -INFINITY, least = INFINITY;
-  int mi = 0, n_live = 0;
-  constexpr int UN = 4;  // pieces in flight
-  for (int c0 = s0_ + int(threadIdx.x) * 8; c0 < s1_; c0 += SA_THREADS * 8 * UN) {
-    SaRaw<T> r[UN];
+__device__ SaFirst Sampler<T>::first_pass(bool want_tail, bool want_z, float cz) {
+  constexpr int STEP = SA_THREADS * 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float m = -INFINITY;
+  int mi = 0x7FFFFFFF, ne = 0;
+  double tail = 0.0, z = 0.0;
+  uint32_t least = 0xFFFFFFFFu;
+  // A ring of copies (cp.async), each thread's own, so that the loads of the
+  // next DEPTH pieces are under way while one is worked on.
+  constexpr int PL = sizeof(T) / 2, DEPTH = SA_RING / (SA_THREADS * 16 * PL);
+  const int cw = s0_ + warp * SA_SEG;  // where the warp's first piece begins
+  const int np = cw < s1_ ? (s1_ - cw + STEP - 1) / STEP : 0;
+  auto slot = [&](int p, int i) {
+    return reinterpret_cast<uint4*>(s_.ring) + ((p % DEPTH) * PL + i) * SA_THREADS + threadIdx.x;
+  };
+  auto issue = [&](int p) {
+    const int c = cw + lane * 8 + p * STEP;
+    if (p < np) {
+      if (a_.vec && c + 8 <= s1_) {
 #pragma unroll
-    for (int k = 0; k < UN; ++k)
-      if (c0 + k * SA_THREADS * 8 < s1_) r[k] = fetch(c0 + k * SA_THREADS * 8);
+        for (int i = 0; i < PL; ++i)
+          asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
+                           smem_u32(slot(p, i))),
+                       "l"(reinterpret_cast<const uint4*>(g_ + c) + i)
+                       : "memory");
+      } else {
+        const SaRaw<T> r = fetch(c);
 #pragma unroll
-    for (int k = 0; k < UN; ++k) {
-      const int c = c0 + k * SA_THREADS * 8;
-      if (c >= s1_) continue;
-      if (a_.resident) {
-#pragma unroll
-        for (int i = 0; i < int(sizeof(T) / 2); ++i) store_[i * plane + (c - s0_) / 8] = r[k].v[i];
+        for (int i = 0; i < PL; ++i) *slot(p, i) = r.v[i];
       }
-      float v[8];
-      raw_values<T>(r[k], v);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int p = 0; p < DEPTH; ++p) issue(p);
+  __syncthreads();  // what run() laid out in shared memory
+  for (int p = 0; p < np; ++p) {
+    const int c = cw + lane * 8 + p * STEP;
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    SaRaw<T> r;
+#pragma unroll
+    for (int i = 0; i < PL; ++i) r.v[i] = *slot(p, i);
+    issue(p + DEPTH);
+    float v[8], vm = -INFINITY;
+    raw_values<T>(r, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) vm = fmaxf(vm, v[j]);  // NaN drops out
+    const uint32_t key = __reduce_max_sync(0xffffffffu, vm > -INFINITY ? value_key(vm) : 0u);
+    if (key == 0) continue;  // nothing live
+    if (lane == 0) {
+      uint32_t* e = &s_.segs[(cw - s0_ + p * STEP) / SA_SEG / a_.seg_mul];
+      if (a_.seg_mul == 1) *e = key;
+      else atomicMax(e, key);
+    }
+    least = min(least, key);
+    const float bm = key_value(key);
+    if (bm > m) {
+      tail = (tail + ne) * ex2_approx((m - bm) * 1.44269504f);
+      z = (z + ne) * ex2_approx(m == -INFINITY ? m : (m - bm) * cz);
+      m = bm;
+      ne = 0;
+      mi = 0x7FFFFFFF;
+    }
+    float st = 0.f, sz = 0.f;
+    if (want_tail) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) st += ex2_approx((v[j] - m) * 1.44269504f);
+    }
+    if (want_z) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sz += ex2_approx((v[j] - m) * cz);
+    }
+    if (vm == m || st != st || sz != sz) {  // the maximum itself, NaN, infinities
+      st = sz = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (v[j] > -INFINITY) {
-          ++n_live;
-          least = fminf(least, v[j]);
-          if (v[j] > m) {
-            m = v[j];
-            mi = c + j;
-          }
+        const float d = v[j] - m;
+        if (v[j] == m) {
+          ++ne;
+          mi = min(mi, c + j);
+        } else if (d > -INFINITY) {
+          st += ex2_approx(d * 1.44269504f);
+          sz += ex2_approx(d * cz);
         }
       }
     }
+    tail += double(st);
+    z += double(sz);
   }
-  SaPart p = nothing();
-  p.n = n_live;
-  p.least = least;
-  if (n_live > 0) p.hi = rank_of(m, mi);
-  p = exchange(p);
+  // threads -> CTA
+  SaFirst f;
+  f.hi = mi != 0x7FFFFFFF ? rank_of(m, mi) : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    f.hi = max(f.hi, __shfl_xor_sync(0xffffffffu, f.hi, o));
+    tail += __shfl_xor_sync(0xffffffffu, tail, o);
+    z += __shfl_xor_sync(0xffffffffu, z, o);
+    ne += __shfl_xor_sync(0xffffffffu, ne, o);
+  }
+  f.tail = tail;
+  f.z = z;
+  f.n = ne;
+  f.least = least == 0xFFFFFFFFu ? INFINITY : key_value(least);
+  if (lane == 0) s_.warp_first[warp] = f;
+  __syncthreads();
+  // The parts of n members, one in each of n lanes, relative to their common
+  // maximum.
+  auto join = [&](SaFirst p, int n) {
+    u64 hi = p.hi;
+    float lo = p.least;
+    for (int o = n / 2; o > 0; o >>= 1) {
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    }
+    if (p.hi == 0) {
+      p.tail = p.z = 0.0;
+      p.n = 0;
+    } else if (p.hi >> 32 != hi >> 32) {
+      const float d = rank_value(p.hi) - rank_value(hi);
+      p.tail = (p.tail + p.n) * ex2_approx(d * 1.44269504f);
+      p.z = (p.z + p.n) * ex2_approx(d == -INFINITY ? d : d * cz);
+      p.n = 0;
+    }
+    for (int o = n / 2; o > 0; o >>= 1) {
+      p.tail += __shfl_xor_sync(0xffffffffu, p.tail, o);
+      p.z += __shfl_xor_sync(0xffffffffu, p.z, o);
+      p.n += __shfl_xor_sync(0xffffffffu, p.n, o);
+    }
+    p.hi = hi;
+    p.least = lo;
+    return p;
+  };
+  if (warp == 0) {
+    f = join(s_.warp_first[lane & (SA_WARPS - 1)], SA_WARPS);
+    if (lane < C_) *cl_.map_shared_rank(&s_.firsts[me_], lane) = f;
+  }
+  cl_.sync();
+  return join(s_.firsts[lane & (C_ - 1)], C_);
+}
+
+template <typename T>
+__device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
+  // Bins between the maximum and the least of the segments' maxima, which
+  // falls short of the last bin; that one takes what is below.
+  const float scale = scale_for(below(f.least)) * 0.996f;
+  int last;  // candidates: the logits in bins up to this one
+  const bool all = a_.V <= SA_CAP;
+  if (all) {
+    last = SA_BINS;
+  } else if (o.use_m && !o.use_p && o.k == 0) {
+    last = int(fmin(floor(-o.thr * (1.0 + 0x1p-20) * double(scale)) + 1.0, double(SA_BINS)));
+  } else {
+    // top-k: the bin of the k-th largest maximum, which k logits reach.
+    // Otherwise: the bin down to which the maxima alone have the mass that is
+    // asked for, or that of the SA_OPEN-th largest, or of the least.
+    if (o.k > SA_CAP / 2) return false;
+    const int n_segs = (s1_ - s0_ + SA_SEG * a_.seg_mul - 1) / (SA_SEG * a_.seg_mul);
+    uint32_t* open = cl_.map_shared_rank(s_.open, 0);
+    for (int i = threadIdx.x; i < n_segs; i += SA_THREADS)
+      if (s_.segs[i] != 0) atomicAdd(&open[bin_below(max_, key_value(s_.segs[i]), scale)], 1u);
+    cl_.sync();
+    const uint4 n4 = reinterpret_cast<const uint4*>(open)[threadIdx.x];
+    const uint32_t n1[4] = {n4.x, n4.y, n4.z, n4.w};
+    const double part = (o.use_p ? double(fmaxf(o.tp, 0.f)) : o.u) * (1.0 + SA_SUM_ERROR);
+    const u64 mass = u64(part * (double(f.n) + f.z) * 0x1p20) + 2;
+    const u64 want = o.k > 0 ? o.k : SA_OPEN;
+    u64 n[4], w[4], sn = 0, sw = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      n[i] = sn += n1[i];
+      // a weight at the bin's far end, rounded down
+      const float x = float(threadIdx.x * 4 + i + 1) / scale * float(-c_);
+      w[i] = sw += n1[i] ? u64(n1[i] * (ex2_approx(x) * 0x1p20f * 0.99f)) : 0;
+    }
+    if (threadIdx.x == 0) s_.bin = s_.done = bin_below(max_, f.least, scale);
+    __syncthreads();
+    const u64 bn = scan(sn, s_.warp_sum[0]) - sn, bw = scan(sw, s_.warp_sum[1]) - sw;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = threadIdx.x * 4 + i;
+      if (bn + n[i] >= want && bn + (i ? n[i - 1] : 0) < want) s_.bin = b;
+      if (o.k == 0 && bw + w[i] >= mass && bw + (i ? w[i - 1] : 0) < mass) s_.done = b;
+    }
+    __syncthreads();
+    last = o.k == 0 ? (s_.done < bin_below(max_, f.least, scale) ? s_.done : s_.bin) : s_.bin;
+    __syncthreads();
+  }
+  // the segments that reach that far, then their logits
+  const int n_rows = (s1_ - s0_ + SA_SEG - 1) / SA_SEG;
+  for (int i = threadIdx.x; i < n_rows; i += SA_THREADS) {
+    const uint32_t key = s_.segs[i / a_.seg_mul];
+    if (key != 0 && bin_below(max_, key_value(key), scale) <= last)
+      s_.opened[atomicAdd(&s_.n_opened, 1)] = uint16_t(i);
+  }
+  __syncthreads();
+  constexpr int UN = 4;
+  const int n_opened = s_.n_opened;
+  for (int i0 = threadIdx.x >> 5; i0 < n_opened; i0 += SA_WARPS * UN) {
+    SaRaw<T> r[UN];
+    int c[UN];
+#pragma unroll
+    for (int k = 0; k < UN; ++k) {
+      const int i = i0 + k * SA_WARPS;
+      c[k] = i < n_opened ? s0_ + int(s_.opened[i]) * SA_SEG + int(threadIdx.x & 31) * 8 : s1_;
+      if (c[k] < s1_) r[k] = fetch(c[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < UN; ++k) {
+      if (c[k] >= s1_) continue;
+      float v[8];
+      raw_values<T>(r[k], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (v[j] > -INFINITY && bin_below(max_, v[j], scale) <= last)
+          append(rank_of(v[j], c[k] + j));
+    }
+  }
+  cl_.sync();
+  if (me_ == 0) {
+    bool ok = s_.n_list <= SA_CAP;
+    if (ok) {
+      const int n = sort_list();
+      u64 r[4], cum[4];
+      const u64 before = running_mass(n, 0, r, cum);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = threadIdx.x * 4 + i;
+        if (q == n - 1) s_.end = cum[i];
+        if (o.k > 0 && q == min(o.k, n) - 1) s_.res_cum = cum[i];
+      }
+      __syncthreads();
+      const u64 end = s_.end;
+      // mass of the kept ranks: exact (lo = hi), or the total from the pass
+      double lo, hi;
+      u64 keep = 0;
+      bool exact = true;
+      if (o.k > 0) {
+        ok = all || n >= o.k;
+        keep = s_.res_cum;
+      } else if (all) {
+        keep = end;
+      } else {
+        exact = false;
+        const double unit = double(u64(1) << a_.bits);
+        lo = (double(f.n) + f.z * (1.0 - SA_SUM_ERROR)) * unit - double(a_.V);
+        hi = (double(f.n) + f.z * (1.0 + SA_SUM_ERROR)) * unit + double(a_.V);
+      }
+      // the rank that both ends of the interval lead to
+      auto settle = [&](u64 a, u64 b) {
+        pick(n, before, r, cum, a);
+        const u64 first = s_.res_rank;
+        if (b != a) pick(n, before, r, cum, b);
+        return b <= end && s_.res_rank == first;
+      };
+      if (ok && o.use_p) {
+        ok = exact ? settle(min(nucleus(o.tp, double(keep)), keep), min(nucleus(o.tp, double(keep)), keep))
+                   : settle(nucleus(o.tp, lo), nucleus(o.tp, hi));
+        keep = exact ? min(keep, s_.res_cum) : s_.res_cum;
+        exact = true;
+      }
+      if (ok && o.use_m) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // the last rank that min_p leaves
+          const int q = threadIdx.x * 4 + i;
+          const bool in = q < n && above_min(rank_value(r[i]), o);
+          if (in && !(q + 1 < n && above_min(rank_value(s_.list[q + 1]), o))) s_.res_cum = cum[i];
+        }
+        __syncthreads();
+        keep = exact ? min(keep, s_.res_cum) : s_.res_cum;
+        exact = true;
+      }
+      if (ok)
+        ok = exact ? settle(part_of(o.u, double(keep)) + 1, part_of(o.u, double(keep)) + 1)
+                   : settle(part_of(o.u, lo) + 1, part_of(o.u, hi) + 1);
+    }
+    __syncthreads();
+    if (int(threadIdx.x) < C_) *cl_.map_shared_rank(&s_.done, threadIdx.x) = ok;
+  }
+  cl_.sync();
+  return s_.done;
+}
+
+template <typename T>
+__device__ void Sampler<T>::by_search(const Settings& o) {
+  // Bins over 40 T: a weight changes by 2 % across one, and those past the
+  // end (the last bin) are below half a unit, exactly 0.
+  bin_scale_ = scale_for(40.f * o.temp);
+  bin_level0();
+  u64 live = 0, keep = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    live += s_.tot[threadIdx.x * 4 + i];
+    keep += s_.mass[threadIdx.x * 4 + i];
+  }
+  live = scan(live, s_.warp_sum[0]);
+  keep = scan(keep, s_.warp_sum[1]);
+  if (threadIdx.x == SA_THREADS - 1) {
+    s_.base = live;
+    s_.end = keep;
+  }
+  __syncthreads();
+  live = s_.base;
+  keep = s_.end;
+  if (o.k > 0 && u64(o.k) < live) {
+    find(false, u64(o.k));
+    const u64 cut = s_.res_rank;
+    keep = mass_of([&](float l, int i) { return rank_of(l, i) >= cut; });
+  }
+  if (o.use_p) {
+    find(true, min(nucleus(o.tp, double(keep)), keep));
+    keep = min(keep, s_.res_cum);
+  }
+  if (o.use_m) keep = min(keep, mass_of([&](float l, int) { return above_min(l, o); }));
+  find(true, part_of(o.u, double(keep)) + 1);
+}
+
+template <typename T>
+template <int MODE>
+__device__ void Sampler<T>::run() {
+  if (MODE == SA_SEARCH_ONLY && a_.token[row_] != SA_UNDECIDED) return;
+  if (threadIdx.x < 32) s_.pow2[threadIdx.x] = exp2(double(threadIdx.x) / 32.0);
+  for (int i = threadIdx.x; i < SA_BINS; i += SA_THREADS) s_.open[i] = 0;
+  for (int i = threadIdx.x; i < SA_MAX_SEGS; i += SA_THREADS) s_.segs[i] = 0;
+  if (threadIdx.x == 0) s_.n_list = s_.n_opened = 0;
+  Settings o;
+  o.temp = a_.temperature == nullptr ? 1.f : a_.temperature[row_];
+  o.k = a_.top_k == nullptr ? 0 : max(a_.top_k[row_], 0);
+  if (o.k >= a_.V) o.k = 0;
+  o.tp = a_.top_p == nullptr ? 1.f : a_.top_p[row_];
+  const float mp = a_.min_p == nullptr ? 0.f : a_.min_p[row_];
+  o.u = double(fminf(fmaxf(a_.u[row_], 0.f), 1.f - 0x1p-24f));
+  o.use_p = o.tp < 1.f;
+  o.use_m = mp > 0.f;
+  o.thr = o.use_m && mp < 1.f ? double(o.temp) * log(double(mp)) : 0.0;
+  const bool greedy = !(o.temp > 0.f) || o.k == 1;
+  const bool need_z =
+      MODE != SA_SEARCH_ONLY && !greedy && o.k == 0 && (o.use_p || !o.use_m);
+  c_ = 1.4426950408889634074 / double(o.temp);
+  const bool same = o.temp == 1.f;  // one sum serves both
+
+  SaFirst f = first_pass(a_.logp != nullptr || (need_z && same), need_z && !same, float(c_));
+  if (same) f.z = f.tail;
   const bool lead = me_ == 0 && threadIdx.x == 0;
-  if (p.n == 0) {
+  if (f.hi == 0) {
     if (lead) {
       a_.token[row_] = -1;
       if (a_.logp != nullptr) a_.logp[row_] = 0.f;
     }
     return;
   }
-  const u64 best = p.hi;
-  const int live = p.n;
-  max_ = rank_value(best);
-
-  const float temp = a_.temperature == nullptr ? 1.f : a_.temperature[row_];
-  const int k = a_.top_k == nullptr ? 0 : a_.top_k[row_];
-  const float tp = a_.top_p == nullptr ? 1.f : a_.top_p[row_];
-  const float mp = a_.min_p == nullptr ? 0.f : a_.min_p[row_];
-  const float u = fminf(fmaxf(a_.u[row_], 0.f), 1.f - 0x1p-24f);
-  const bool greedy = !(temp > 0.f) || k == 1 || live == 1;
-  const bool use_k = k > 0 && k < live, use_p = tp < 1.f, use_m = mp > 0.f;
-  const bool need_z = !greedy && !use_k && (use_p || !use_m);
-  c_ = 1.4426950408889634074 / double(temp);
-  // Bins over 40 T: a weight changes by 2 % across one, and those past the
-  // end (the last bin) are below half a unit, exactly 0.
-  bin_scale_ = scale_for(fminf(below(p.least), 40.f * temp));
-
-  // Pass 2: counts by bin, the sum behind logp, the total mass.
-  p = nothing();
-  if (!greedy) clear_hist();
-  if (!greedy || a_.logp != nullptr) {
-    const int skip = rank_index(best);
-    pass([&](const float (&v)[8], int c) {
-      float tail = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (!(v[j] > -INFINITY)) continue;
-        if (c + j != skip) tail += ex2_approx(-below(v[j]) * 1.44269504f);
-        if (!greedy) atomicAdd(&s_.hist[bin_of(v[j])], 1u);
-        if (need_z) p.mass += weight(v[j]);
-      }
-      p.tail += double(tail);
-    });
-    p = exchange(p);
-  }
-  const u64 z = p.mass;
-  const double lse = log1p(p.tail);  // log sum exp(l - max)
-  u64 token = best;
+  max_ = rank_value(f.hi);
+  u64 token = f.hi;
   if (!greedy) {
-    total_hist(s_.tot);
-    const double thr = use_m && mp < 1.f ? double(temp) * log(double(mp)) : 0.0;
-    auto above_min = [&](float l) { return -(l == max_ ? 0.0 : double(max_) - double(l)) >= thr; };
-    // Which ranks can the first filter (or the draw itself) reach?
-    const bool by_mass = !use_k;
-    u64 target;
-    if (use_k) target = u64(k);
-    else if (use_p) target = max(u64(1), min(z, u64(ceil(double(tp) * double(z)))));
-    else target = part_of(double(u), z) + 1;
-    bool in_list;
-    int last_bin;
-    if (!use_k && !use_p && use_m) {
-      last_bin = int(min(floor(-thr * (1.0 + 0x1p-20) * double(bin_scale_)) + 1.0,
-                         double(SA_BINS - 1)));
-      u64 n = 0;
-      for (int i = 0; i < 4; ++i)
-        if (int(threadIdx.x) * 4 + i <= last_bin) n += s_.tot[threadIdx.x * 4 + i];
-      n = scan(n, s_.warp_sum[0]);
-      if (threadIdx.x == SA_THREADS - 1) s_.n_in = uint32_t(n);
-      __syncthreads();
-      in_list = s_.n_in <= SA_CAP;
-    } else {
-      bracket(s_.tot, by_mass, target, [&](int b, bool up) { return edge(b, up, max_, bin_scale_); });
-      last_bin = s_.hi_bin;
-      in_list = s_.n_above + s_.n_in <= SA_CAP;
+    const bool done = MODE != SA_SEARCH_ONLY && by_list(o, f);
+    if (!done) {
+      if (MODE == SA_LIST_ONLY) {
+        if (lead) a_.token[row_] = SA_UNDECIDED;
+        return;
+      }
+      by_search(o);
     }
-    if (in_list) {
-      // Everything that can be kept fits the list: the first CTA finishes.
-      if (threadIdx.x == 0) s_.n_list = 0;
-      __syncthreads();
-      pass([&](const float (&v)[8], int c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (v[j] > -INFINITY && bin_of(v[j]) <= last_bin) append(rank_of(v[j], c + j));
-      });
-      const int n = gather_sorted();
-      if (me_ == 0) {
-        u64 r[4], cum[4];
-        const u64 before = running_mass(n, 0, r, cum);
-        u64 keep = z;  // mass of the kept ranks
-        if (use_k) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (int(threadIdx.x) * 4 + i == min(k, n) - 1) s_.res_cum = cum[i];
-          __syncthreads();
-          keep = s_.res_cum;
-        }
-        if (use_p) {
-          const u64 t = max(u64(1), min(keep, u64(ceil(double(tp) * double(keep)))));
-          pick(n, before, r, cum, t);
-          keep = min(keep, s_.res_cum);
-        }
-        if (use_m) {
-          __syncthreads();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // the last rank above the threshold
-            const int q = threadIdx.x * 4 + i;
-            const bool in = q < n && above_min(rank_value(r[i]));
-            const bool next = q + 1 < n && above_min(rank_value(s_.list[q + 1]));
-            if (in && !next) s_.res_cum = cum[i];
-          }
-          __syncthreads();
-          keep = use_k || use_p ? min(keep, s_.res_cum) : s_.res_cum;
-        }
-        pick(n, before, r, cum, part_of(double(u), keep) + 1);
-        token = s_.res_rank;
-      }
-    } else {
-      u64 keep = z;
-      if (use_k) {
-        find(false, u64(k));
-        const u64 cut = s_.res_rank;
-        keep = mass_of([&](float l, int i) { return rank_of(l, i) >= cut; });
-      }
-      if (use_p) {
-        find(true, max(u64(1), min(keep, u64(ceil(double(tp) * double(keep))))));
-        keep = min(keep, s_.res_cum);
-      }
-      if (use_m) {
-        const u64 w = mass_of([&](float l, int) { return above_min(l); });
-        keep = use_k || use_p ? min(keep, w) : w;
-      }
-      find(true, part_of(double(u), keep) + 1);
-      token = s_.res_rank;
-    }
+    token = s_.res_rank;
   }
   if (lead) {
     a_.token[row_] = rank_index(token);
-    if (a_.logp != nullptr) a_.logp[row_] = float(-double(below(rank_value(token))) - lse);
+    if (a_.logp != nullptr)
+      a_.logp[row_] =
+          float(-double(below(rank_value(token))) - log1p(f.tail + double(f.n - 1)));
   }
-  cl_.sync();  // shared memory stays until every CTA has read it
 }
 
-template <typename T>
-__global__ void __launch_bounds__(SA_THREADS) sample_kernel(SampleArgs a) {
-  extern __shared__ uint4 sa_store[];
-  __shared__ SaShared s;
-  Sampler<T> sampler(a, s, sa_store);
-  __syncthreads();
-  sampler.run();
+template <typename T, int MODE>
+__global__ void __launch_bounds__(SA_THREADS, 2) sample_kernel(SampleArgs a) {
+  extern __shared__ __align__(16) uint8_t sa_smem[];
+  Sampler<T>(a, *reinterpret_cast<SaShared*>(sa_smem)).template run<MODE>();
 }
 
 }  // namespace cce
