@@ -163,7 +163,10 @@ cce_status launch_sample(SampleArgs a, int64_t B, int c, cudaStream_t st) {
   a.slice = int(ceil_div(ceil_div(a.V, c), SA_SEG)) * SA_SEG;
   a.seg_mul = int(ceil_div(a.slice / SA_SEG, SA_MAX_SEGS));
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(B) * c);
+  // the search: as many clusters as run at once
+  const int64_t rows = MODE == SA_SEARCH_ONLY
+                           ? std::min<int64_t>(B, std::max(1, 2 * sm_count_guess() / c)) : B;
+  cfg.gridDim = dim3(unsigned(rows) * c);
   cfg.blockDim = dim3(SA_THREADS);
   cfg.dynamicSmemBytes = sizeof(SaShared);
   cfg.stream = st;
@@ -425,6 +428,7 @@ cce_status cce_sample_rows(const void* logits, cce_dtype dtype, int64_t B, int64
   std::memset(&a, 0, sizeof(a));
   a.logits = logits;
   a.ld = ld;
+  a.B = int(B);
   a.V = int(V);
   a.vec = rows16(logits, ld, dtype_bytes(dtype));
   int log2v = 0;

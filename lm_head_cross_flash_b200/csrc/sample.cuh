@@ -15,7 +15,7 @@
 //
 // Two ways.  A cluster of CTAs takes a row.  One pass over memory gives the
 // maximum, sums of fp32 exponentials (behind logp, and the total mass to a
-// known error) and the largest logit of every segment of 256.
+// known error) and the largest logit of every segment of 512.
 //  * List.  Nearly always the kept ranks are few.  The segments' maxima say
 //    below which value enough ranks, or enough mass, must lie; only segments
 //    that reach it are read again, and the candidates are sorted by the
@@ -46,12 +46,13 @@ constexpr int SA_WARPS = SA_THREADS / 32;
 constexpr int SA_BINS = 2048;
 constexpr int SA_CAP = 2048;  // candidates of one list
 constexpr int SA_MAX_CLUSTER = 8;
-constexpr int SA_SEG = 256;        // logits that a warp reads at once: one segment
+constexpr int SA_SEG = 512;        // logits that a warp reads at once: one segment
 constexpr int SA_MAX_SEGS = 1024;  // segments (or groups of them) of one CTA
-constexpr int SA_OPEN = 256;       // segments that the list opens if their mass is not enough
+constexpr int SA_OPEN = 128;       // segments that the list opens if their mass is not enough
 constexpr int SA_RING = 64 * 1024; // copies in flight during the first pass
 constexpr int SA_FLUSH = 65536;    // logits that 15-bit digits can be summed over in 32 bits
-constexpr int SA_UNDECIDED = -2;   // token of a row that the first launch leaves to the second
+constexpr int SA_UNDECIDED = -2;   // token of a row that the first launch leaves to the second,
+constexpr int SA_CLAIMED = -3;     // and of one that a cluster of the second works on
 enum : int { SA_BOTH = 0, SA_LIST_ONLY = 1, SA_SEARCH_ONLY = 2 };  // what a launch does
 static_assert(SA_CAP == 4 * SA_THREADS && SA_BINS == 4 * SA_THREADS, "four entries per thread");
 
@@ -64,7 +65,7 @@ constexpr double SA_SUM_ERROR = 0x1p-16;
 struct SampleArgs {
   const void* logits;
   int64_t ld;
-  int V;
+  int B, V;
   int slice;    // logits per CTA, a multiple of SA_SEG
   int seg_mul;  // segments that share an entry of segs[]
   int vec;      // rows start on 16-byte boundaries
@@ -133,6 +134,7 @@ struct SaShared {
   int bin;
   int n_list, n_opened;
   int done;  // the list gave the answer
+  int row;   // the search's
 };
 
 template <typename T>
@@ -160,11 +162,11 @@ __device__ __forceinline__ void raw_values(const SaRaw<T>& r, float (&v)[8]) {
 template <typename T>
 class Sampler {
  public:
-  __device__ Sampler(const SampleArgs& a, SaShared& s)
+  __device__ Sampler(const SampleArgs& a, SaShared& s, int row)
       : a_(a), s_(s), cl_(cooperative_groups::this_cluster()) {
     C_ = int(cl_.num_blocks());
     me_ = int(cl_.block_rank());
-    row_ = int(blockIdx.x) / C_;
+    row_ = row;
     g_ = static_cast<const T*>(a.logits) + int64_t(row_) * a.ld;
     s0_ = int(min(int64_t(a.V), int64_t(me_) * a.slice));
     s1_ = int(min(int64_t(a.V), int64_t(s0_) + a.slice));
@@ -467,7 +469,13 @@ class Sampler {
     return s < 1e30f ? s : 1e30f;
   }
 
-  __device__ SaFirst first_pass(bool want_tail, bool want_z, float cz);
+  template <bool TAIL, bool Z>
+  __device__ SaFirst first_pass(float cz);
+  // 2^(c m - h): what a weight of 1 is in sums that are relative to h.
+  __device__ static double unround(float m, float c, float h) {
+    const float d = fmaf(m, c, -h);
+    return fabsf(d) < 1.f ? 1.0 + double(d) * 0.6931471805599453 : 1.0;
+  }
   struct Settings {
     float temp, tp;
     int k;
@@ -586,38 +594,52 @@ __device__ void Sampler<T>::find(bool by_mass, u64 target) {
   share_result();
 }
 
-// The logits come in once.  Every warp keeps its own running maximum, so the
-// sums are relative to that until the end.
+// Largest of the lanes' values; NaN drops out.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The logits come in once.  Every warp keeps its own running maximum m, and
+// its sums are relative to that until the end.  An exponential is one FMA and
+// one ex2: 2^(c l - h) with h = c m rounded; the sums are put right by
+// 2^(h - c m) at the end (the difference is the same for all terms).
 template <typename T>
-__device__ SaFirst Sampler<T>::first_pass(bool want_tail, bool want_z, float cz) {
-  constexpr int STEP = SA_THREADS * 8;
+template <bool TAIL, bool Z>
+__device__ SaFirst Sampler<T>::first_pass(float cz) {
+  constexpr int STEP = SA_WARPS * SA_SEG, NB = SA_SEG / 256;
+  constexpr float CT = 1.44269504f;  // log2(e)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float m = -INFINITY;
+  float m = -INFINITY, ht = 0.f, hz = 0.f, least = INFINITY;
   int mi = 0x7FFFFFFF, ne = 0;
   double tail = 0.0, z = 0.0;
-  uint32_t least = 0xFFFFFFFFu;
   // A ring of copies (cp.async), each thread's own, so that the loads of the
-  // next DEPTH pieces are under way while one is worked on.
-  constexpr int PL = sizeof(T) / 2, DEPTH = SA_RING / (SA_THREADS * 16 * PL);
-  const int cw = s0_ + warp * SA_SEG;  // where the warp's first piece begins
+  // next DEPTH segments are under way while one is worked on.  A segment is
+  // NB pieces of 256: eight logits a lane.
+  constexpr int PL = sizeof(T) / 2, DEPTH = SA_RING / (SA_THREADS * 16 * PL * NB);
+  static_assert(DEPTH >= 2 && (DEPTH & (DEPTH - 1)) == 0, "a power of two");
+  const int cw = s0_ + warp * SA_SEG;  // where the warp's first segment begins
   const int np = cw < s1_ ? (s1_ - cw + STEP - 1) / STEP : 0;
-  auto slot = [&](int p, int i) {
-    return reinterpret_cast<uint4*>(s_.ring) + ((p % DEPTH) * PL + i) * SA_THREADS + threadIdx.x;
-  };
+  const int full = a_.vec && s1_ - cw >= SA_SEG ? (s1_ - cw - SA_SEG) / STEP + 1 : 0;
+  uint4* const ring = reinterpret_cast<uint4*>(s_.ring) + threadIdx.x;
+  auto slot = [&](int p) { return ring + (p & (DEPTH - 1)) * (NB * PL * SA_THREADS); };
   auto issue = [&](int p) {
-    const int c = cw + lane * 8 + p * STEP;
-    if (p < np) {
-      if (a_.vec && c + 8 <= s1_) {
+    if (p < full) {
+      const uint32_t to = smem_u32(slot(p));
+      const uint4* from = reinterpret_cast<const uint4*>(g_ + cw + p * STEP + lane * 8);
 #pragma unroll
-        for (int i = 0; i < PL; ++i)
-          asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
-                           smem_u32(slot(p, i))),
-                       "l"(reinterpret_cast<const uint4*>(g_ + c) + i)
-                       : "memory");
-      } else {
-        const SaRaw<T> r = fetch(c);
+      for (int i = 0; i < NB * PL; ++i)
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
+                         to + i * SA_THREADS * 16),
+                     "l"(from + (i / PL) * 32 * PL + i % PL)
+                     : "memory");
+    } else if (p < np) {
 #pragma unroll
-        for (int i = 0; i < PL; ++i) *slot(p, i) = r.v[i];
+      for (int k = 0; k < NB; ++k) {
+        const SaRaw<T> r = fetch(cw + p * STEP + k * 256 + lane * 8);
+#pragma unroll
+        for (int i = 0; i < PL; ++i) slot(p)[(k * PL + i) * SA_THREADS] = r.v[i];
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -625,58 +647,77 @@ __device__ SaFirst Sampler<T>::first_pass(bool want_tail, bool want_z, float cz)
   for (int p = 0; p < DEPTH; ++p) issue(p);
   __syncthreads();  // what run() laid out in shared memory
   for (int p = 0; p < np; ++p) {
-    const int c = cw + lane * 8 + p * STEP;
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-    SaRaw<T> r;
+    float v[NB][8], vm = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) r.v[i] = *slot(p, i);
-    issue(p + DEPTH);
-    float v[8], vm = -INFINITY;
-    raw_values<T>(r, v);
+    for (int k = 0; k < NB; ++k) {
+      SaRaw<T> r;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) vm = fmaxf(vm, v[j]);  // NaN drops out
-    const uint32_t key = __reduce_max_sync(0xffffffffu, vm > -INFINITY ? value_key(vm) : 0u);
-    if (key == 0) continue;  // nothing live
-    if (lane == 0) {
-      uint32_t* e = &s_.segs[(cw - s0_ + p * STEP) / SA_SEG / a_.seg_mul];
-      if (a_.seg_mul == 1) *e = key;
-      else atomicMax(e, key);
+      for (int i = 0; i < PL; ++i) r.v[i] = slot(p)[(k * PL + i) * SA_THREADS];
+      raw_values<T>(r, v[k]);
     }
-    least = min(least, key);
-    const float bm = key_value(key);
+    issue(p + DEPTH);
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vm = fmaxf(vm, v[k][j]);  // NaN drops out
+    const float bm = warp_max(vm);
+    if (bm == -INFINITY) continue;  // nothing live
+    if (lane == 0) {
+      const int seg = warp + p * SA_WARPS;
+      if (a_.seg_mul == 1) s_.segs[seg] = value_key(bm);
+      else atomicMax(&s_.segs[seg / a_.seg_mul], value_key(bm));
+    }
+    least = fminf(least, bm);
     if (bm > m) {
-      tail = (tail + ne) * ex2_approx((m - bm) * 1.44269504f);
-      z = (z + ne) * ex2_approx(m == -INFINITY ? m : (m - bm) * cz);
+      // the sums so far, and the instances of the old maximum, in the new scale
+      const float nt = bm * CT, nz = bm * cz;
+      if (m > -INFINITY) {
+        if (TAIL) tail = (tail + double(ne) * unround(m, CT, ht)) * double(ex2_approx(ht - nt));
+        if (Z) z = bm == INFINITY ? 0.0 : (z + double(ne) * unround(m, cz, hz)) * double(ex2_approx(hz - nz));
+      }
       m = bm;
+      ht = nt;
+      hz = nz;
       ne = 0;
       mi = 0x7FFFFFFF;
     }
-    float st = 0.f, sz = 0.f;
-    if (want_tail) {
+    float st[NB] = {}, sz[NB] = {};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) st += ex2_approx((v[j] - m) * 1.44269504f);
-    }
-    if (want_z) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sz += ex2_approx((v[j] - m) * cz);
-    }
-    if (vm == m || st != st || sz != sz) {  // the maximum itself, NaN, infinities
-      st = sz = 0.f;
+    for (int k = 0; k < NB; ++k)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = v[j] - m;
-        if (v[j] == m) {
-          ++ne;
-          mi = min(mi, c + j);
-        } else if (d > -INFINITY) {
-          st += ex2_approx(d * 1.44269504f);
-          sz += ex2_approx(d * cz);
-        }
+        if (TAIL) st[k] += ex2_approx(fmaf(v[k][j], CT, -ht));
+        if (Z) sz[k] += ex2_approx(fmaf(v[k][j], cz, -hz));
       }
+    float sum_t = st[0], sum_z = sz[0];
+#pragma unroll
+    for (int k = 1; k < NB; ++k) {
+      sum_t += st[k];
+      sum_z += sz[k];
     }
-    tail += double(st);
-    z += double(sz);
+    if (vm == m || sum_t != sum_t || sum_z != sum_z) {  // the maximum itself, NaN, infinities
+      sum_t = sum_z = 0.f;
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float l = v[k][j];
+          if (l == m) {
+            ++ne;
+            mi = min(mi, cw + p * STEP + k * 256 + lane * 8 + j);
+          } else if (l - m > -INFINITY) {
+            const float x = fmaf(l, CT, -ht), y = fmaf(l, cz, -hz);
+            sum_t += ex2_approx(x);
+            sum_z += y == y ? ex2_approx(y) : 0.f;
+          }
+        }
+    }
+    if (TAIL) tail += double(sum_t);
+    if (Z) z += double(sum_z);
   }
+  tail /= unround(m, CT, ht);
+  z /= unround(m, cz, hz);
   // threads -> CTA
   SaFirst f;
   f.hi = mi != 0x7FFFFFFF ? rank_of(m, mi) : 0;
@@ -690,7 +731,7 @@ __device__ SaFirst Sampler<T>::first_pass(bool want_tail, bool want_z, float cz)
   f.tail = tail;
   f.z = z;
   f.n = ne;
-  f.least = least == 0xFFFFFFFFu ? INFINITY : key_value(least);
+  f.least = least;
   if (lane == 0) s_.warp_first[warp] = f;
   __syncthreads();
   // The parts of n members, one in each of n lanes, relative to their common
@@ -783,15 +824,18 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
       s_.opened[atomicAdd(&s_.n_opened, 1)] = uint16_t(i);
   }
   __syncthreads();
-  constexpr int UN = 4;
+  constexpr int UN = 4, NB = SA_SEG / 256;
   const int n_opened = s_.n_opened;
-  for (int i0 = threadIdx.x >> 5; i0 < n_opened; i0 += SA_WARPS * UN) {
+  for (int i0 = threadIdx.x >> 5; i0 < n_opened * NB; i0 += SA_WARPS * UN) {
     SaRaw<T> r[UN];
     int c[UN];
 #pragma unroll
     for (int k = 0; k < UN; ++k) {
       const int i = i0 + k * SA_WARPS;
-      c[k] = i < n_opened ? s0_ + int(s_.opened[i]) * SA_SEG + int(threadIdx.x & 31) * 8 : s1_;
+      // a piece of 256 of each
+      c[k] = i < n_opened * NB ? s0_ + int(s_.opened[i / NB]) * SA_SEG + i % NB * 256 +
+                                     int(threadIdx.x & 31) * 8
+                               : s1_;
       if (c[k] < s1_) r[k] = fetch(c[k]);
     }
 #pragma unroll
@@ -908,7 +952,6 @@ __device__ void Sampler<T>::by_search(const Settings& o) {
 template <typename T>
 template <int MODE>
 __device__ void Sampler<T>::run() {
-  if (MODE == SA_SEARCH_ONLY && a_.token[row_] != SA_UNDECIDED) return;
   if (threadIdx.x < 32) s_.pow2[threadIdx.x] = exp2(double(threadIdx.x) / 32.0);
   for (int i = threadIdx.x; i < SA_BINS; i += SA_THREADS) s_.open[i] = 0;
   for (int i = threadIdx.x; i < SA_MAX_SEGS; i += SA_THREADS) s_.segs[i] = 0;
@@ -929,7 +972,10 @@ __device__ void Sampler<T>::run() {
   c_ = 1.4426950408889634074 / double(o.temp);
   const bool same = o.temp == 1.f;  // one sum serves both
 
-  SaFirst f = first_pass(a_.logp != nullptr || (need_z && same), need_z && !same, float(c_));
+  const bool tail = a_.logp != nullptr || (need_z && same);
+  SaFirst f = need_z && !same ? (tail ? first_pass<true, true>(float(c_))
+                                      : first_pass<false, true>(float(c_)))
+                              : (tail ? first_pass<true, false>(0.f) : first_pass<false, false>(0.f));
   if (same) f.z = f.tail;
   const bool lead = me_ == 0 && threadIdx.x == 0;
   if (f.hi == 0) {
@@ -960,10 +1006,43 @@ __device__ void Sampler<T>::run() {
   }
 }
 
+// One cluster a row; the search's clusters take rows that are left, each when
+// it is done with its last (the rows cost very different times).
 template <typename T, int MODE>
 __global__ void __launch_bounds__(SA_THREADS, 2) sample_kernel(SampleArgs a) {
   extern __shared__ __align__(16) uint8_t sa_smem[];
-  Sampler<T>(a, *reinterpret_cast<SaShared*>(sa_smem)).template run<MODE>();
+  SaShared& s = *reinterpret_cast<SaShared*>(sa_smem);
+  const int n = int(cluster_count_x()), id = int(cluster_id_x());
+  if (MODE != SA_SEARCH_ONLY) {
+    Sampler<T>(a, s, id).template run<MODE>();
+    return;
+  }
+  auto cluster = cooperative_groups::this_cluster();
+  const int start = int(int64_t(a.B) * id / n), lane = threadIdx.x & 31;
+  for (;;) {
+    if (cluster.block_rank() == 0 && threadIdx.x < 32) {
+      int row = -1;
+      for (int i = 0; i < a.B && row < 0; i += 32) {
+        const int q = (start + i + lane) % a.B;
+        // not every lane's load is needed, and a lane may see a row twice
+        const bool left = i + lane < a.B && ld_relaxed_gpu(reinterpret_cast<const uint32_t*>(
+                                                a.token + q)) == uint32_t(SA_UNDECIDED);
+        for (uint32_t some = __ballot_sync(0xffffffffu, left); some != 0 && row < 0;
+             some &= some - 1) {
+          const int q0 = __shfl_sync(0xffffffffu, q, __ffs(some) - 1);
+          int got = 0;
+          if (lane == 0) got = atomicCAS(a.token + q0, SA_UNDECIDED, SA_CLAIMED) == SA_UNDECIDED;
+          if (__shfl_sync(0xffffffffu, got, 0)) row = q0;
+        }
+      }
+      if (lane < int(cluster.num_blocks())) *cluster.map_shared_rank(&s.row, lane) = row;
+    }
+    cluster.sync();
+    const int row = s.row;
+    if (row < 0) return;
+    Sampler<T>(a, s, row).template run<MODE>();
+    cluster.sync();  // the row's shared memory is done with
+  }
 }
 
 }  // namespace cce
