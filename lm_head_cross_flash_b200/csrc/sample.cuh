@@ -189,46 +189,82 @@ class Sampler {
 
   // ------------------------------------------------------------- passes --
   __device__ SaRaw<T> fetch(int c) const {
+    if (!a_.vec || c + 8 > s1_) return fetch_ragged(g_, c, s1_);
     SaRaw<T> r;
-    if (a_.vec && c + 8 <= s1_) {
 #pragma unroll
-      for (int i = 0; i < int(sizeof(T) / 2); ++i)
-        r.v[i] = __ldg(reinterpret_cast<const uint4*>(g_ + c) + i);
-    } else {  // -inf behind the end
-      uint32_t w[sizeof(T) * 2];
-#pragma unroll
-      for (int i = 0; i < int(sizeof(T) * 2); ++i) {
-        if constexpr (sizeof(T) == 4) {
-          w[i] = c + i < s1_ ? __float_as_uint(g_[c + i]) : 0xFF800000u;
-        } else {
-          const uint32_t lo = c + 2 * i < s1_ ? __bfloat16_as_ushort(g_[c + 2 * i]) : 0xFF80u;
-          const uint32_t hi = c + 2 * i + 1 < s1_ ? __bfloat16_as_ushort(g_[c + 2 * i + 1]) : 0xFF80u;
-          w[i] = lo | (hi << 16);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < int(sizeof(T) / 2); ++i)
-        r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    }
+    for (int i = 0; i < int(sizeof(T) / 2); ++i)
+      r.v[i] = __ldg(reinterpret_cast<const uint4*>(g_ + c) + i);
     return r;
   }
-  // Calls f(values, first index) on every piece of eight logits in [from, to)
-  // (from: a multiple of 8 in the slice).
-  template <typename F>
-  __device__ void pass(int from, int to, F f) const {
-    constexpr int STEP = SA_THREADS * 8, UN = sizeof(T) == 4 ? 2 : 4;
-    for (int c0 = from + int(threadIdx.x) * 8; c0 < to; c0 += STEP * UN) {
-      SaRaw<T> r[UN];
+  // -inf behind the end
+  __device__ static __noinline__ SaRaw<T> fetch_ragged(const T* g, int c, int end) {
+    SaRaw<T> r;
+    uint32_t w[sizeof(T) * 2];
 #pragma unroll
-      for (int k = 0; k < UN; ++k)
-        if (c0 + k * STEP < to) r[k] = fetch(c0 + k * STEP);
-#pragma unroll
-      for (int k = 0; k < UN; ++k) {
-        if (c0 + k * STEP >= to) break;
-        float v[8];
-        raw_values<T>(r[k], v);
-        f(v, c0 + k * STEP);
+    for (int i = 0; i < int(sizeof(T) * 2); ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = c + i < end ? __float_as_uint(g[c + i]) : 0xFF800000u;
+      } else {
+        const uint32_t lo = c + 2 * i < end ? __bfloat16_as_ushort(g[c + 2 * i]) : 0xFF80u;
+        const uint32_t hi = c + 2 * i + 1 < end ? __bfloat16_as_ushort(g[c + 2 * i + 1]) : 0xFF80u;
+        w[i] = lo | (hi << 16);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i)
+      r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    return r;
+  }
+  __device__ int n_segs() const { return (s1_ - s0_ + SA_SEG - 1) / SA_SEG; }
+  // Calls f(values, first index) on every piece of eight logits in the
+  // segments [from, to) whose largest logit's key passes want().  One piece is
+  // loaded ahead; not unrolled (the callers' code for eight logits is long,
+  // and four copies of it did not fit the instruction cache: 16 % of the
+  // search's warp cycles).
+  template <typename W, typename F>
+  __device__ void pass(int from, int to, W want, F f) const {
+    constexpr int NB = SA_SEG / 256;
+    const int lane8 = int(threadIdx.x & 31) * 8;
+    auto skip = [&](int i) {  // the first wanted segment from i on
+      for (; i < to; i += SA_WARPS) {
+        const uint32_t key = s_.segs[a_.seg_mul == 1 ? i : i / a_.seg_mul];
+        if (key != 0 && want(key)) break;
+      }
+      return i;
+    };
+    int i = skip(from + int(threadIdx.x >> 5)), k = 0;
+    if (i >= to) return;
+    int c = s0_ + i * SA_SEG + lane8;
+    SaRaw<T> r = fetch(c);
+#pragma unroll 1
+    while (i < to) {
+      if (++k == NB) {
+        k = 0;
+        i = skip(i + SA_WARPS);
+      }
+      const int next = s0_ + i * SA_SEG + k * 256 + lane8;
+      SaRaw<T> ahead = r;
+      if (i < to) ahead = fetch(next);
+      float v[8];
+      raw_values<T>(r, v);
+      f(v, c);
+      c = next;
+      r = ahead;
+    }
+  }
+  template <typename F>
+  __device__ void pass(F f) const {
+    pass(0, n_segs(), [](uint32_t) { return true; }, f);
+  }
+  // The logits of a piece that hit() takes, one by one (few of many).
+  template <typename H, typename F>
+  __device__ void each_hit(const float (&v)[8], int c, H hit, F f) const {
+    uint32_t mask = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mask |= uint32_t(v[j] > -INFINITY && hit(v[j], c + j)) << j;
+    for (; mask != 0; mask &= mask - 1) {
+      const int j = __ffs(mask) - 1;
+      f(rank_of(to_f32(g_[c + j]), c + j));
     }
   }
 
@@ -301,10 +337,10 @@ class Sampler {
     return x;
   }
   // Counts (and, by_mass, weights) of the logits by bin, of the whole cluster:
-  // bin(value, index) < 0 leaves a logit out.  Barriers of the cluster on both
-  // sides.
-  template <typename F>
-  __device__ void bin_up(bool by_mass, F bin) {
+  // bin(value, index) < 0 leaves a logit out, as it does all of a segment
+  // whose maximum's key want() refuses.  Ends with a barrier of the cluster.
+  template <typename W, typename F>
+  __device__ void bin_up(bool by_mass, W want, F bin) {
     auto clear = [&](bool counts) {
       for (int i = threadIdx.x; i < SA_BINS; i += SA_THREADS) {
         if (counts) s_.hist[i] = 0;
@@ -318,10 +354,10 @@ class Sampler {
     clear(true);
     const int n = SA_BINS / C_, b0 = me_ * n;  // the bins that this CTA adds up
     u64 sum[SA_BINS / SA_THREADS] = {};
-    const int end = s0_ + a_.slice;  // the same number of rounds in every CTA
-    for (int c0 = s0_; c0 < end; c0 += SA_FLUSH) {
+    const int end = a_.slice / SA_SEG;  // the same number of rounds in every CTA
+    for (int from = 0; from < end; from += SA_FLUSH / SA_SEG) {
       __syncthreads();
-      pass(c0, min(s1_, c0 + SA_FLUSH), [&](const float (&v)[8], int c) {
+      pass(from, min(n_segs(), from + SA_FLUSH / SA_SEG), want, [&](const float (&v)[8], int c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (!(v[j] > -INFINITY)) continue;
@@ -344,7 +380,7 @@ class Sampler {
         for (int q = 0; q < SA_BINS / SA_THREADS; ++q)
           if (q == k) sum[q] += x;
       }
-      if (c0 + SA_FLUSH < end) {
+      if (from + SA_FLUSH / SA_SEG < end) {
         cl_.sync();
         clear(false);
       }
@@ -365,7 +401,7 @@ class Sampler {
   }
 
   __device__ void bin_level0() {
-    bin_up(true, [&](float l, int) { return bin_of(l); });
+    bin_up(true, [](uint32_t) { return true; }, [&](float l, int) { return bin_of(l); });
     level0_ = true;
   }
 
@@ -398,36 +434,74 @@ class Sampler {
     const int i = atomicAdd(cl_.map_shared_rank(&s_.n_list, 0), 1);
     if (i < SA_CAP) cl_.map_shared_rank(s_.list, 0)[i] = r;
   }
-  // First CTA: sorts the list from the highest rank down; its length.
-  __device__ int sort_list() {
-    const int n = min(s_.n_list, SA_CAP);
-    int len = 2;
+  // First CTA: sorts the list from the highest rank down; its length.  Thread
+  // t gets the ranks 4t to 4t + 3.  A bitonic network: strides below 4 stay in
+  // a thread, those below 128 in a warp (shuffles), the others go through the
+  // list's memory.
+  __device__ int sort_list(u64 (&r)[4]) {
+    const int n = min(s_.n_list, SA_CAP), e0 = threadIdx.x * 4;
+    int len = 128;
     while (len < n) len *= 2;
-    for (int i = n + int(threadIdx.x); i < len; i += SA_THREADS) s_.list[i] = 0;
+    const bool in = e0 < len;  // the same for a whole warp
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = e0 + i < n ? s_.list[e0 + i] : 0;
     __syncthreads();
+    if (threadIdx.x == 0) s_.n_list = 0;  // for the next list
+    auto order = [](u64& x, u64& y, bool down) {
+      const u64 a = x, b = y;
+      if ((a < b) == down) {
+        x = b;
+        y = a;
+      }
+    };
     for (int k = 2; k <= len; k *= 2)
       for (int j = k / 2; j > 0; j /= 2) {
-        for (int t = threadIdx.x; t < len / 2; t += SA_THREADS) {
-          const int i = 2 * t - (t & (j - 1)), o = i + j;
-          const u64 x = s_.list[i], y = s_.list[o];
-          if ((x < y) == ((i & k) == 0)) {
-            s_.list[i] = y;
-            s_.list[o] = x;
+        if (j >= 128) {
+          if (in) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s_.list[e0 + i] = r[i];
           }
+          __syncthreads();
+          if (in) {
+            const bool most = ((e0 & k) == 0) == ((e0 & j) == 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const u64 o = s_.list[(e0 ^ j) + i];
+              r[i] = most ? max(r[i], o) : min(r[i], o);
+            }
+          }
+          __syncthreads();
+        } else if (!in) {
+          continue;
+        } else if (j >= 4) {
+          const bool most = ((e0 & k) == 0) == ((e0 & j) == 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const u64 o = __shfl_xor_sync(0xffffffffu, r[i], j / 4);
+            r[i] = most ? max(r[i], o) : min(r[i], o);
+          }
+        } else if (j == 2) {
+          order(r[0], r[2], (e0 & k) == 0);
+          order(r[1], r[3], (e0 & k) == 0);
+        } else {
+          order(r[0], r[1], (e0 & k) == 0);
+          order(r[2], r[3], ((e0 + 2) & k) == 0);
         }
-        __syncthreads();
       }
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s_.list[e0 + i] = r[i];
+    }
+    __syncthreads();
     return n;
   }
-  // First CTA: the four sorted candidates of this thread with the masses up
-  // to and including each, above `base`.  Returns the mass before the first.
-  __device__ u64 running_mass(int n, u64 base, u64 (&r)[4], u64 (&cum)[4]) {
+  // First CTA: the masses up to and including each of this thread's sorted
+  // candidates, above `base`.  Returns the mass before the first.
+  __device__ u64 running_mass(int n, u64 base, const u64 (&r)[4], u64 (&cum)[4]) {
     u64 sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int k = threadIdx.x * 4 + i;
-      r[i] = k < n ? s_.list[k] : 0;
-      sum += k < n ? weight(rank_value(r[i])) : 0;
+      sum += int(threadIdx.x) * 4 + i < n ? weight(rank_value(r[i])) : 0;
       cum[i] = sum;
     }
     const u64 before = base + scan(sum, s_.warp_sum[0]) - sum;
@@ -491,15 +565,26 @@ class Sampler {
   // Both set res_rank to the chosen rank; by_list returns false if it cannot
   // be sure of it.
   __device__ bool by_list(const Settings& o, const SaFirst& f);
-  __device__ __noinline__ void by_search(const Settings& o);
+  __device__ void by_search(const Settings& o);
   // The rank at which the running count (by_mass: mass) reaches the target
   // (at least 1, at most the total): res_rank, and by mass res_cum.
-  __device__ __noinline__ void find(bool by_mass, u64 target);
+  // Not inlined (three calls): works on a copy, so that the members stay in
+  // registers.
+  __device__ void find(bool by_mass, u64 target) {
+    const int was = find_apart(*this, by_mass, target);
+    turn_ = was & 1;
+    level0_ = was >> 1;
+  }
+  __device__ static __noinline__ int find_apart(Sampler me, bool by_mass, u64 target) {
+    me.search(by_mass, target);
+    return me.turn_ | (me.level0_ ? 2 : 0);
+  }
+  __device__ void search(bool by_mass, u64 target);
   // Mass of the logits for which keep(value, index) holds.
   template <typename F>
   __device__ u64 mass_of(F keep) {
     SaPart p = nothing();
-    pass(s0_, s1_, [&](const float (&v)[8], int c) {
+    pass([&](const float (&v)[8], int c) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (v[j] > -INFINITY && keep(v[j], c + j)) p.mass += weight(v[j]);
@@ -512,7 +597,7 @@ class Sampler {
 };
 
 template <typename T>
-__device__ void Sampler<T>::find(bool by_mass, u64 target) {
+__device__ void Sampler<T>::search(bool by_mass, u64 target) {
   u64 top = ~u64(0), bottom = 0, base = 0;  // the ranks searched; the measure above them
   float vt = max_, scale = bin_scale_;      // their bins: by value,
   int shift = -1;                           // or by index (one value)
@@ -522,32 +607,33 @@ __device__ void Sampler<T>::find(bool by_mass, u64 target) {
   for (int step = 0; step < 64; ++step) {
     const u64 top0 = top, bottom0 = bottom;
     auto bin = [&](float l, int i) {
+      if (step == 0) return bin_of(l);
       const u64 r = rank_of(l, i);
       if (r > top0 || r < bottom0) return -1;
       return shift >= 0 ? int((top0 - r) >> shift) : bin_below(vt, l, scale);
     };
     if (step > 0)  // the first bins are there already
-      bin_up(by_mass, bin);
+      bin_up(by_mass, [&](uint32_t key) { return key >= uint32_t(bottom0 >> 32); }, bin);
     locate(by_mass, target - base);
     base += s_.base;
     fits = s_.n_in <= SA_CAP;
     const int here = s_.bin;
-    if (threadIdx.x == 0) s_.n_list = 0;
-    cl_.sync();
     SaPart p = nothing();
-    pass(s0_, s1_, [&](const float (&v)[8], int c) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (!(v[j] > -INFINITY) || bin(v[j], c + j) != here) continue;
-        const u64 r = rank_of(v[j], c + j);
-        if (fits) {
-          append(r);
-        } else {
-          p.hi = max(p.hi, r);
-          p.lo = min(p.lo, r);
-        }
-      }
-    });
+    pass(
+        0, n_segs(),
+        [&](uint32_t key) {
+          return step == 0 ? bin_of(key_value(key)) <= here : key >= uint32_t(bottom0 >> 32);
+        },
+        [&](const float (&v)[8], int c) {
+          each_hit(v, c, [&](float l, int i) { return bin(l, i) == here; }, [&](u64 r) {
+            if (fits) {
+              append(r);
+            } else {
+              p.hi = max(p.hi, r);
+              p.lo = min(p.lo, r);
+            }
+          });
+        });
     if (fits) break;
     p = exchange(p);
     top = p.hi;
@@ -555,7 +641,7 @@ __device__ void Sampler<T>::find(bool by_mass, u64 target) {
     if (top - bottom > (top0 - bottom0) / 2) {
       const u64 mid = bottom + (top - bottom) / 2;
       p = nothing();
-      pass(s0_, s1_, [&](const float (&v)[8], int c) {
+      pass([&](const float (&v)[8], int c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (!(v[j] > -INFINITY)) continue;
@@ -582,9 +668,10 @@ __device__ void Sampler<T>::find(bool by_mass, u64 target) {
   }
   cl_.sync();
   if (me_ == 0) {
-    const int n = sort_list();
+    u64 r[4];
+    const int n = sort_list(r);
     if (by_mass) {
-      u64 r[4], cum[4];
+      u64 cum[4];
       const u64 before = running_mass(n, base, r, cum);
       pick(n, before, r, cum, target);
     } else if (threadIdx.x == 0 && n > 0) {
@@ -785,9 +872,9 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
     // Otherwise: the bin down to which the maxima alone have the mass that is
     // asked for, or that of the SA_OPEN-th largest, or of the least.
     if (o.k > SA_CAP / 2) return false;
-    const int n_segs = (s1_ - s0_ + SA_SEG * a_.seg_mul - 1) / (SA_SEG * a_.seg_mul);
+    const int n_maxima = (n_segs() + a_.seg_mul - 1) / a_.seg_mul;
     uint32_t* open = cl_.map_shared_rank(s_.open, 0);
-    for (int i = threadIdx.x; i < n_segs; i += SA_THREADS)
+    for (int i = threadIdx.x; i < n_maxima; i += SA_THREADS)
       if (s_.segs[i] != 0) atomicAdd(&open[bin_below(max_, key_value(s_.segs[i]), scale)], 1u);
     cl_.sync();
     const uint4 n4 = reinterpret_cast<const uint4*>(open)[threadIdx.x];
@@ -817,8 +904,7 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
     __syncthreads();
   }
   // the segments that reach that far, then their logits
-  const int n_rows = (s1_ - s0_ + SA_SEG - 1) / SA_SEG;
-  for (int i = threadIdx.x; i < n_rows; i += SA_THREADS) {
+  for (int i = threadIdx.x; i < n_segs(); i += SA_THREADS) {
     const uint32_t key = s_.segs[i / a_.seg_mul];
     if (key != 0 && bin_below(max_, key_value(key), scale) <= last)
       s_.opened[atomicAdd(&s_.n_opened, 1)] = uint16_t(i);
@@ -843,18 +929,16 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
       if (c[k] >= s1_) continue;
       float v[8];
       raw_values<T>(r[k], v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (v[j] > -INFINITY && bin_below(max_, v[j], scale) <= last)
-          append(rank_of(v[j], c[k] + j));
+      each_hit(v, c[k], [&](float l, int) { return bin_below(max_, l, scale) <= last; },
+               [&](u64 q) { append(q); });
     }
   }
   cl_.sync();
   if (me_ == 0) {
     bool ok = s_.n_list <= SA_CAP;
     if (ok) {
-      const int n = sort_list();
       u64 r[4], cum[4];
+      const int n = sort_list(r);
       const u64 before = running_mass(n, 0, r, cum);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -909,6 +993,7 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
                    : settle(part_of(o.u, lo) + 1, part_of(o.u, hi) + 1);
     }
     __syncthreads();
+    if (threadIdx.x == 0) s_.n_list = 0;  // it may have run over
     if (int(threadIdx.x) < C_) *cl_.map_shared_rank(&s_.done, threadIdx.x) = ok;
   }
   cl_.sync();
@@ -917,9 +1002,9 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
 
 template <typename T>
 __device__ void Sampler<T>::by_search(const Settings& o) {
-  // Bins over 40 T: a weight changes by 2 % across one, and those past the
-  // end (the last bin) are below half a unit, exactly 0.
-  bin_scale_ = scale_for(40.f * o.temp);
+  // Bins over 24 T: what lies below has less than 4e-11 of the largest weight
+  // each, and falls into the last bin.
+  bin_scale_ = scale_for(24.f * o.temp);
   bin_level0();
   u64 live = 0, keep = 0;
 #pragma unroll
@@ -1006,10 +1091,13 @@ __device__ void Sampler<T>::run() {
   }
 }
 
-// One cluster a row; the search's clusters take rows that are left, each when
+// 128 registers a thread where the search runs: with 64 (two CTAs on an SM) it
+// spilled, and one row took 17 us instead of 13 by list and 51 instead of 35 by
+// search.  One cluster a row; the search's clusters take rows that are left, each when
 // it is done with its last (the rows cost very different times).
 template <typename T, int MODE>
-__global__ void __launch_bounds__(SA_THREADS, 2) sample_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(SA_THREADS, MODE == SA_LIST_ONLY ? 2 : 1)
+    sample_kernel(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t sa_smem[];
   SaShared& s = *reinterpret_cast<SaShared*>(sa_smem);
   const int n = int(cluster_count_x()), id = int(cluster_id_x());
