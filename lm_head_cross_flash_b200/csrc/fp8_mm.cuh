@@ -8,8 +8,8 @@
 // scales, to fp32 sums in registers.  That costs one tensor-memory read and
 // one FMA per partial; both run beside the next group's MMAs.
 //
-// fp8_rows_kernel: any number of rows; 128 rows x 256 columns of C per CTA,
-//   row tiles fastest, so the CTAs in flight share the same rows of b.
+// fp8_rows_kernel: any number of rows; 256 x 256 tiles of C by CTA pairs, row
+//   tiles fastest, so the CTAs in flight share the same rows of b.
 // fp8_few_kernel: up to 128 rows (decoding).  The roles of the operands are
 //   exchanged: 128 rows of b are the MMA's M side and the few rows of a its N
 //   side, so a pass over b costs no idle tensor rows; the CTAs of a cluster
@@ -87,23 +87,103 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, uint32_t mask, uint
 }
 
 // ----------------------------------------------------------- many rows --
+// A pair of CTAs makes a 256 x 256 tile with tcgen05.mma.cta_group::2: each
+// CTA loads its 128 rows of a and half of the 256 rows of b, so a group costs
+// it 32 KB of shared-memory writes and as much of reads (48 KB each for 128 x
+// 256 tiles of single CTAs, whose 768 cycles of shared memory stood against
+// 512 of MMAs).  Both copies complete on the leader's barrier, only the leader
+// issues MMAs; no copy is multicast.
+//
+// Warps 0 and 1 copy and issue; warps 4 to 11 drain, one row and 128 columns
+// (one 128-block of b, so one scale) a thread.  128 sums and two buffers of 32
+// partials need more registers than an even share, so the first warpgroup
+// hands its own over (setmaxnreg: 128 * 56 + 256 * 224 = 384 * 168).
 constexpr int F8_BM = 128, F8_BN = 256, F8_BK = 128;
-constexpr int F8_STAGES = 4;
-constexpr int F8_STAGE = (F8_BM + F8_BN) * F8_BK;
-constexpr int F8_THREADS = 320;  // copies, MMA, 8 epilogue warps
+constexpr int F8_STAGES = 5;
+constexpr int F8_STAGE = (F8_BM + F8_BN / 2) * F8_BK;
+constexpr int F8_THREADS = 384;
+constexpr int F8_REGS = 168, F8_REGS_ISSUE = 56, F8_REGS_DRAIN = 224;
+static_assert(128 * F8_REGS_ISSUE + 256 * F8_REGS_DRAIN <= F8_THREADS * F8_REGS, "registers");
+constexpr int F8_OUT = 8 * 32 * 128;  // a 32 x 128-byte block for each draining warp
 using F8Sync = Fp8Sync<F8_STAGES, 2>;
-constexpr int F8_SMEM = F8_STAGES * F8_STAGE + sizeof(F8Sync) + 1024;
+constexpr int F8_SMEM = F8_STAGES * F8_STAGE + F8_OUT + sizeof(F8Sync) + 1024;
+
+__device__ __forceinline__ void umma_e4m3_ss2(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the pair leader's barrier without a fence of cluster scope: what
+// is handed over is tensor memory whose reads have completed
+// (tcgen05.wait::ld), no memory.  With .release.cluster the draining warps
+// spent a third of their time in that fence (2048 x 128256 x 4096: 1890 us).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// Two FMAs at once: c += (lo, hi) * s2.
+__device__ __forceinline__ void fma2(uint64_t& c, uint32_t lo, uint32_t hi, uint64_t s2) {
+  asm("{\n\t.reg .b64 x;\n\tmov.b64 x, {%1, %2};\n\tfma.rn.f32x2 %0, x, %3, %0;\n\t}"
+      : "+l"(c)
+      : "r"(lo), "r"(hi), "l"(s2));
+}
+__device__ __forceinline__ float2 unpack2(uint64_t c) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(c));
+  return f;
+}
+
+// 32 rows x (128 / sizeof(T)) columns of a warp go out through shared memory:
+// each lane writes its row (16-byte pieces, swizzled by row), then the warp
+// writes rows of C in whole 128-byte lines.
+template <typename T>
+__device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t* sm, int row0, int col0,
+                                            const uint4 (&piece)[8]) {
+  const int lane = threadIdx.x & 31;
+  constexpr int NC = 128 / sizeof(T);
+  T* const c = static_cast<T*>(a.c);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    *reinterpret_cast<uint4*>(sm + lane * 128 + ((i ^ (lane & 7)) << 4)) = piece[i];
+  __syncwarp();
+  if (a.vec && col0 + NC <= a.N) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3), k = lane & 7;
+      const uint4 v = *reinterpret_cast<const uint4*>(sm + r * 128 + ((k ^ (r & 7)) << 4));
+      if (row0 + r < a.M)
+        *reinterpret_cast<uint4*>(c + (row0 + r) * a.ldc + col0 + k * (16 / sizeof(T))) = v;
+    }
+  } else {
+    const int rows = min(32, a.M - row0);
+    for (int r = 0; r < rows; ++r)
+#pragma unroll
+      for (int h = 0; h < NC / 32; ++h) {
+        const int j = h * 32 + lane, at = j * int(sizeof(T));
+        const T v = *reinterpret_cast<const T*>(sm + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
+        if (col0 + j < a.N) c[(row0 + r) * a.ldc + col0 + j] = v;
+      }
+  }
+  __syncwarp();
+}
 
 __global__ void __launch_bounds__(F8_THREADS, 1)
     fp8_rows_kernel(const __grid_constant__ CUtensorMap tmA,
-                    const __grid_constant__ CUtensorMap tmB, Fp8Args a) {
+                    const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ Fp8Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  F8Sync* sy = reinterpret_cast<F8Sync*>(base + F8_STAGES * F8_STAGE);
+  uint8_t* const out = base + F8_STAGES * F8_STAGE;
+  F8Sync* sy = reinterpret_cast<F8Sync*>(out + F8_OUT);
   volatile int* abort_flag = &sy->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(cluster_ctarank());
   const int ntiles = a.n_rt * a.n_ct;
+  const int tile0 = int(cluster_id_x()), tstep = int(cluster_count_x());
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < F8_STAGES; ++s) {
@@ -112,21 +192,23 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sy->acc_full[b], 1);
-      mbar_init(&sy->acc_empty[b], 8);
+      mbar_init(&sy->acc_empty[b], 16);  // the draining warps of both CTAs
     }
     mbar_init(&sy->drain, 1);
     sy->abort = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(&sy->tmem, 512);
-    tmem_relinquish();
+    tmem_alloc2(&sy->tmem, 512);
+    tmem_relinquish2();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // barriers of both CTAs initialised
   tc_fence_after();
   const uint32_t tmem = sy->tmem;
 
+  // Row tiles fastest inside a group of row tiles that stays in L2.
   auto tile_at = [&](int t, int& rt, int& ct) {
     const int per_group = a.group_rt * a.n_ct;
     const int grp = t / per_group, r = t - grp * per_group;
@@ -135,13 +217,14 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     ct = r / gn;
   };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F8_REGS_ISSUE));
+    if (warp == 0 && lane == 0) {
       int stage = 0;
       uint32_t phase = 0, mask = 0, phases = 0;
       bool ok = true;
-      const uint64_t keep = l2_policy_evict_last();
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      const uint64_t keep = l2_policy_evict_last(), once = l2_policy_evict_normal();
+      for (int t = tile0; t < ntiles && ok; t += tstep) {
         int rt, ct;
         tile_at(t, rt, ct);
         for (int g = 0; g < a.G; ++g) {
@@ -150,9 +233,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             break;
           }
           uint8_t* s = base + stage * F8_STAGE;
-          mbar_arrive_expect_tx(&sy->full[stage], F8_STAGE);
-          tma_load_2d_hint(s, &tmA, &sy->full[stage], g * F8_BK, rt * F8_BM, keep);
-          tma_load_2d(s + F8_BM * F8_BK, &tmB, &sy->full[stage], g * F8_BK, ct * F8_BN);
+          const uint32_t bar = mapa_shared(smem_u32(&sy->full[stage]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&sy->full[stage], 2 * F8_STAGE);
+          tma_load_2d_pair(s, &tmA, bar, g * F8_BK, (rt * 2 + rank) * F8_BM, keep);
+          tma_load_2d_pair(s + F8_BM * F8_BK, &tmB, bar, g * F8_BK,
+                           ct * F8_BN + rank * (F8_BN / 2), once);
           mask |= 1u << stage;
           phases = (phases & ~(1u << stage)) | (phase << stage);
           if (++stage == F8_STAGES) {
@@ -165,15 +250,14 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         set_status(a.status, ST_TIMEOUT);
         *abort_flag = 1;
       }
-      drain_copies<F8_STAGES>(sy->full, mask, phases);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(F8_BM, F8_BN);
+      // the leader's barriers count the other CTA's copies too
+      if (rank == 0) drain_copies<F8_STAGES>(sy->full, mask, phases);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(2 * F8_BM, F8_BN);
       int stage = 0;
       uint32_t phase = 0, acc = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      for (int t = tile0; t < ntiles && ok; t += tstep) {
         for (int g = 0; g < a.G; ++g, ++acc) {
           const int b = acc & 1;
           if (!wait_bounded(&sy->acc_empty[b], ((acc >> 1) & 1) ^ 1u, a.wait_ns, abort_flag) ||
@@ -185,10 +269,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           const uint32_t sA = smem_u32(base + stage * F8_STAGE), sB = sA + F8_BM * F8_BK;
 #pragma unroll
           for (int j = 0; j < F8_BK / 32; ++j)
-            umma_e4m3_ss(tmem + b * F8_BN, sdesc_sw128(sA + j * 32, 16, 1024),
-                         sdesc_sw128(sB + j * 32, 16, 1024), idesc, j != 0);
-          umma_commit(&sy->empty[stage]);
-          umma_commit(&sy->acc_full[b]);
+            umma_e4m3_ss2(tmem + b * F8_BN, sdesc_sw128(sA + j * 32, 16, 1024),
+                          sdesc_sw128(sB + j * 32, 16, 1024), idesc, j != 0);
+          umma_commit2_mc(&sy->empty[stage], 0x3);
+          umma_commit2_mc(&sy->acc_full[b], 0x3);
           if (++stage == F8_STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -200,48 +284,56 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         *abort_flag = 1;
       }
       // the MMAs of this thread complete before tensor memory is released
-      umma_commit(&sy->drain);
+      umma_commit2_mc(&sy->drain, 0x1);
       wait_bounded(&sy->drain, 0, 1000000000ull, nullptr);
     }
   } else {
-    // One row of C and 128 of its columns per thread.
-    const int quad = warp & 3, half = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8_REGS_DRAIN));
+    const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+    uint8_t* const sm = out + (warp - 4) * 4096;
+    const uint32_t empty0 = mapa_shared(smem_u32(&sy->acc_empty[0]), 0);
+    const uint32_t empty1 = mapa_shared(smem_u32(&sy->acc_empty[1]), 0);
     uint32_t acc = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+    for (int t = tile0; t < ntiles; t += tstep) {
       int rt, ct;
       tile_at(t, rt, ct);
-      const int row = rt * F8_BM + quad * 32 + lane, col = ct * F8_BN + half * 128;
-      const float* psa = a.sa + static_cast<size_t>(min(row, a.M - 1)) * a.G;
+      const int row0 = (rt * 2 + rank) * F8_BM + quad * 32, col = ct * F8_BN + half * 128;
+      const float* psa = a.sa + static_cast<size_t>(min(row0 + lane, a.M - 1)) * a.G;
       const float* psb = a.sb + static_cast<size_t>(min(col, a.N - 1) / QGROUP) * a.G;
-      float c[128];
+      uint64_t c[64];
 #pragma unroll
-      for (int j = 0; j < 128; ++j) c[j] = 0.f;
-      float sc = __ldg(psa) * __ldg(psb);
+      for (int j = 0; j < 64; ++j) c[j] = 0;
+      float sa = __ldg(psa), sb = __ldg(psb);
+      bool ok = true;
       for (int g = 0; g < a.G; ++g, ++acc) {
         const int b = acc & 1;
-        const float s = sc;
+        const float s = sa * sb;
+        uint64_t s2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
         const int gn = min(g + 1, a.G - 1);
-        sc = __ldg(psa + gn) * __ldg(psb + gn);
+        sa = __ldg(psa + gn);
+        sb = __ldg(psb + gn);
         if (!wait_bounded(&sy->acc_full[b], (acc >> 1) & 1, a.wait_ns, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t r[2][16];
-        tmem_ld16(taddr + b * F8_BN, r[0]);
+        uint32_t r[2][32];
+        tmem_ld32(taddr + b * F8_BN, r[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          tmem_ld_wait16(r[i & 1]);
-          if (i < 7) tmem_ld16(taddr + b * F8_BN + (i + 1) * 16, r[(i + 1) & 1]);
+        for (int i = 0; i < 4; ++i) {
+          tmem_ld_wait(r[i & 1]);
+          if (i < 3) {
+            tmem_ld32(taddr + b * F8_BN + (i + 1) * 32, r[(i + 1) & 1]);
+          } else {
+            tc_fence_before();  // all of the partial sums are in registers
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(b ? empty1 : empty0);
+          }
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            c[i * 16 + j] = fmaf(__uint_as_float(r[i & 1][j]), s, c[i * 16 + j]);
+          for (int j = 0; j < 16; ++j) fma2(c[i * 16 + j], r[i & 1][2 * j], r[i & 1][2 * j + 1], s2);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sy->acc_empty[b]);
       }
       if (!ok) {
         if (lane == 0) {
@@ -250,30 +342,35 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         }
         break;
       }
-      if (row < a.M) {
-        const bool vec = a.vec && col + 128 <= a.N;
-        if (a.c_bf16) {
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.c) + row * a.ldc + col;
-          if (vec) {
+      if (row0 >= a.M || col >= a.N) continue;
+      if (a.c_bf16) {
 #pragma unroll
-            for (int j = 0; j < 128; j += 8)
-              store8<true>(out, j, 128, *reinterpret_cast<const float(*)[8]>(&c[j]));
-          } else {
+        for (int h = 0; h < 2; ++h) {
+          uint4 piece[8];
 #pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (col + j < a.N) out[j] = __float2bfloat16_rn(c[j]);
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = unpack2(c[h * 32 + i * 4 + j]);
+              const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
+              w[j] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            piece[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        } else {
-          float* out = static_cast<float*>(a.c) + row * a.ldc + col;
-          if (vec) {
+          store_block<__nv_bfloat16>(a, sm, row0, col + h * 64, piece);
+        }
+      } else {
 #pragma unroll
-            for (int j = 0; j < 128; j += 8)
-              store8<true>(out, j, 128, *reinterpret_cast<const float(*)[8]>(&c[j]));
-          } else {
+        for (int h = 0; h < 4; ++h) {
+          uint4 piece[8];
 #pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (col + j < a.N) out[j] = c[j];
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = unpack2(c[h * 16 + i * 2]), e = unpack2(c[h * 16 + i * 2 + 1]);
+            piece[i] = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y),
+                                  __float_as_uint(e.x), __float_as_uint(e.y));
           }
+          store_block<float>(a, sm, row0, col + h * 32, piece);
         }
       }
     }
@@ -281,10 +378,12 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  // a CTA stays until both are done with each other's barriers and memory
+  cluster_sync_all();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc2(tmem, 512);
   }
 }
 

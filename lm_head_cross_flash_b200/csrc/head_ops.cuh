@@ -405,17 +405,36 @@ cce_status cce_fp8_matmul(const uint8_t* A, int64_t lda, const float* SA, const 
   static bool done[64];
   s = set_smem_once(fp8_rows_kernel, F8_SMEM, done);
   if (s != CCE_OK) return s;
-  a.n_rt = int(ceil_div(M, F8_BM));
+  // the kernel's register hand-over counts on what it is launched with
+  static const int regs = [] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, fp8_rows_kernel) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs != F8_REGS) return CCE_ERR_CUDA;
+  a.n_rt = int(ceil_div(M, 2 * F8_BM));
   a.n_ct = int(ceil_div(N, F8_BN));
   // row tiles of one raster group: 48 MB of A, so that a group stays in L2
   // while the columns pass
   a.group_rt = int(std::max<int64_t>(
-      1, std::min<int64_t>(a.n_rt, (int64_t(48) << 20) / (F8_BM * K))));
+      1, std::min<int64_t>(a.n_rt, (int64_t(48) << 20) / (2 * F8_BM * K))));
   CUtensorMap ma, mb;
-  if (!make_fp8_map(&ma, A, M, K, lda, F8_BM) || !make_fp8_map(&mb, B, N, K, ldb, F8_BN))
+  if (!make_fp8_map(&ma, A, M, K, lda, F8_BM) || !make_fp8_map(&mb, B, N, K, ldb, F8_BN / 2))
     return CCE_ERR_CUDA;
-  fp8_rows_kernel<<<grid_for(int64_t(a.n_rt) * a.n_ct, sms), F8_THREADS, F8_SMEM, st>>>(ma, mb, a);
-  return launch_ok();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * grid_for(int64_t(a.n_rt) * a.n_ct, sms / 2));
+  cfg.blockDim = dim3(F8_THREADS);
+  cfg.dynamicSmemBytes = F8_SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fp8_rows_kernel, ma, mb, a) == cudaSuccess
+             ? launch_ok()
+             : (cudaGetLastError(), CCE_ERR_CUDA);
 }
 
 cce_status cce_sample_rows(const void* logits, cce_dtype dtype, int64_t B, int64_t V, int64_t ld,
