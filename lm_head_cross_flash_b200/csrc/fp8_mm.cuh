@@ -159,13 +159,22 @@ __device__ __forceinline__ void store_block(const Fp8Args& a, uint8_t* sm, int r
     }
   } else {
     const int rows = min(32, a.M - row0);
-    for (int r = 0; r < rows; ++r)
 #pragma unroll
-      for (int h = 0; h < NC / 32; ++h) {
-        const int j = h * 32 + lane, at = j * int(sizeof(T));
-        const T v = *reinterpret_cast<const T*>(sm + r * 128 + (((at >> 4) ^ (r & 7)) << 4) + (at & 15));
-        if (col0 + j < a.N) c[(row0 + r) * a.ldc + col0 + j] = v;
+    for (int h = 0; h < NC / 32; ++h) {
+      const int j = h * 32 + lane, at = j * int(sizeof(T));
+      T* const p = c + row0 * a.ldc + col0 + j;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 8) {
+        T v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = *reinterpret_cast<const T*>(sm + (r0 + i) * 128 + (((at >> 4) ^ i) << 4) + (at & 15));
+        T* q = p + r0 * a.ldc;
+#pragma unroll
+        for (int i = 0; i < 8; ++i, q += a.ldc)
+          if (r0 + i < rows && col0 + j < a.N) *q = v[i];
       }
+    }
   }
   __syncwarp();
 }
