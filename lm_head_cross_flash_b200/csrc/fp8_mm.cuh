@@ -98,6 +98,14 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, uint32_t mask, uint
 // (one 128-block of b, so one scale) a thread.  128 sums and two buffers of 32
 // partials need more registers than an even share, so the first warpgroup
 // hands its own over (setmaxnreg: 128 * 56 + 256 * 224 = 384 * 168).
+//
+// What bounds it (2048 x 18944 x 4096, codes and scales constant): 135 us in
+// all, 105 with the partials left alone, 105 with the MMAs left out, so each
+// side is near the other's time and the hand-over between them is what is
+// left.  Measured against this form: fma.rn.f32 instead of f32x2 1255 us (2048
+// x 128256 x 4096, 1013 here), tiles of 256 x 128 with four accumulators 1343,
+// halves of 128 columns with accumulators of their own 1148, sixteen draining
+// warps 1614 (the instructions that are not FMAs add up).
 constexpr int F8_BM = 128, F8_BN = 256, F8_BK = 128;
 constexpr int F8_STAGES = 5;
 constexpr int F8_STAGE = (F8_BM + F8_BN / 2) * F8_BK;
@@ -269,8 +277,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       for (int t = tile0; t < ntiles && ok; t += tstep) {
         for (int g = 0; g < a.G; ++g, ++acc) {
           const int b = acc & 1;
-          if (!wait_bounded(&sy->acc_empty[b], ((acc >> 1) & 1) ^ 1u, a.wait_ns, abort_flag) ||
-              !wait_bounded(&sy->full[stage], phase, a.wait_ns, abort_flag)) {
+          // the accumulator comes back last: everything else is done by then
+          if (!wait_bounded(&sy->full[stage], phase, a.wait_ns, abort_flag) ||
+              !wait_bounded(&sy->acc_empty[b], ((acc >> 1) & 1) ^ 1u, a.wait_ns, abort_flag)) {
             ok = false;
             break;
           }
@@ -280,8 +289,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           for (int j = 0; j < F8_BK / 32; ++j)
             umma_e4m3_ss2(tmem + b * F8_BN, sdesc_sw128(sA + j * 32, 16, 1024),
                           sdesc_sw128(sB + j * 32, 16, 1024), idesc, j != 0);
-          umma_commit2_mc(&sy->empty[stage], 0x3);
           umma_commit2_mc(&sy->acc_full[b], 0x3);
+          umma_commit2_mc(&sy->empty[stage], 0x3);
           if (++stage == F8_STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -578,17 +587,18 @@ __global__ void __launch_bounds__(FfCfg<NP>::THREADS, 1)
         break;
       }
       if (S == 1) {
-        const int n = t * 128 + vrow;
+        const int n = t * 128 + vrow, m0 = half * NC;
         if (n < a.N) {
+          if (a.c_bf16) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.c) + m0 * a.ldc + n;
 #pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            const int m = half * NC + j;
-            if (m < a.M) {
-              if (a.c_bf16)
-                static_cast<__nv_bfloat16*>(a.c)[m * a.ldc + n] = __float2bfloat16_rn(c[j]);
-              else
-                static_cast<float*>(a.c)[m * a.ldc + n] = c[j];
-            }
+            for (int j = 0; j < NC; ++j, out += a.ldc)
+              if (m0 + j < a.M) *out = __float2bfloat16_rn(c[j]);
+          } else {
+            float* out = static_cast<float*>(a.c) + m0 * a.ldc + n;
+#pragma unroll
+            for (int j = 0; j < NC; ++j, out += a.ldc)
+              if (m0 + j < a.M) *out = c[j];
           }
         }
       } else {
