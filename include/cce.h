@@ -524,7 +524,7 @@ cce_status cce_forward_noalloc(const void* H, int64_t M, const cce_head* W,
  * 8-bit format ("e4m3 groups of 128").  A group holds e4m3 codes q and one
  * fp32 scale s; the values are q * s.  With m = max(2^-90, max |x| over the
  * group),
- *   s = m / 448,   q = e4m3(x * (448 * (1 / m))),
+ *   s = m * (1 / 448),   q = e4m3(x * (448 * (1 / m))),
  * quotients and products rounded in fp32, codes to nearest even.  A
  * group is 128 consecutive columns of a row (activations, checkpoints; scales
  * [M, ceil(D/128)], dense) or a 128 x 128 block (weights; scales

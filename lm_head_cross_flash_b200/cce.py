@@ -735,3 +735,99 @@ def cce_sample_rows(logits, temperature, top_k, top_p, min_p, u, tokens, logp=No
          None if min_p is None else _dense("min_p", min_p, _F32, row, dev),
          _dense("u", u, _F32, row, dev), _dense("tokens", tokens, _I32, row, dev),
          None if logp is None else _dense("logp", logp, _F32, row, dev))
+
+
+# ----------------------------------------------------------------------------
+# the operators in use: training behind a final norm, and decoding
+# ----------------------------------------------------------------------------
+
+@dataclass
+class NormBuffers:
+    """Device buffers of the final norm in a training pass: the head's rows,
+    the 8-bit checkpoint that stands for X until the backward, the gradients
+    (``dW`` None for a frozen norm) and the workspace."""
+
+    H: torch.Tensor
+    X8: torch.Tensor
+    Xs: torch.Tensor
+    rstd: torch.Tensor
+    dX: torch.Tensor
+    dW: torch.Tensor | None
+    ws: torch.Tensor | None
+
+    @staticmethod
+    def alloc(M: int, D: int, H_dtype: int = CCE_BF16, dX_dtype=torch.bfloat16, frozen=False,
+              device="cuda"):
+        f = dict(device=device, dtype=torch.float32)
+        return NormBuffers(
+            H=torch.empty(M, D, device=device,
+                          dtype=torch.float32 if H_dtype == CCE_F32 else torch.bfloat16),
+            X8=fp8_empty(M, D, device), Xs=torch.empty(M, fp8_groups(D), **f),
+            rstd=torch.empty(M, **f), dX=torch.empty(M, D, device=device, dtype=dX_dtype),
+            dW=None if frozen else torch.empty(D, **f),
+            ws=None if frozen else torch.zeros(cce_norm_backward_workspace_bytes(M, D),
+                                               dtype=torch.uint8, device=device))
+
+
+def orpo_norm_head_pass(X, norm_w, eps, head: Head, labels, layout, lam, sft_scope, filter_eps,
+                        block_skip: bool, norm: NormBuffers, buf: HeadBuffers, stream=None):
+    """``orpo_head_pass`` from the residual stream X [M, D] on: the final norm
+    with its 8-bit checkpoint, the head's pass, and the norm's gradient from
+    the checkpoint (``norm.dX``, ``norm.dW``).  X is read by the first kernel
+    only; its memory may be reused once that has run."""
+    cce_norm_forward(X, norm_w, eps, H=norm.H, X8=norm.X8, Xs=norm.Xs, rstd=norm.rstd,
+                     stream=stream)
+    orpo_head_pass(norm.H, head, labels, layout, lam, sft_scope, filter_eps, block_skip, buf,
+                   stream)
+    cce_norm_backward(norm.X8, norm.Xs, norm.rstd, norm_w, buf.dH, norm.dX, norm.dW, norm.ws,
+                      stream)
+
+
+@dataclass
+class Fp8Head:
+    """A dense head in 8 bits for decoding: codes [V, D] and one scale for each
+    128 x 128 block."""
+
+    q: torch.Tensor
+    s: torch.Tensor
+
+    @staticmethod
+    def from_dense(w, stream=None):
+        V, D = w.shape
+        h = Fp8Head(fp8_empty(V, D, w.device),
+                    torch.empty(fp8_groups(V), fp8_groups(D), dtype=torch.float32,
+                                device=w.device))
+        cce_fp8_quant_blocks(w, h.q, h.s, stream)
+        return h
+
+
+@dataclass
+class DecodeBuffers:
+    """Device buffers of one decoding step of B rows."""
+
+    H8: torch.Tensor
+    Hs: torch.Tensor
+    logits: torch.Tensor
+    tokens: torch.Tensor
+    logp: torch.Tensor
+    ws: torch.Tensor
+
+    @staticmethod
+    def alloc(B: int, head: Fp8Head, logits_dtype=torch.float32):
+        (V, D), dev = head.q.shape, head.q.device
+        f = dict(device=dev, dtype=torch.float32)
+        return DecodeBuffers(
+            H8=fp8_empty(B, D, dev), Hs=torch.empty(B, fp8_groups(D), **f),
+            logits=torch.empty(B, V, device=dev, dtype=logits_dtype),
+            tokens=torch.empty(B, dtype=torch.int32, device=dev), logp=torch.empty(B, **f),
+            ws=torch.zeros(256, dtype=torch.uint8, device=dev))
+
+
+def decode_step(X, norm_w, eps, head: Fp8Head, u, buf: DecodeBuffers, temperature=None,
+                top_k=None, top_p=None, min_p=None, stream=None):
+    """The last step of decoding for B rows of the residual stream: final norm
+    into 8 bits, logits, one sampled token a row (``buf.tokens``, and
+    ``buf.logp``, the log-prob that the ORPO loss takes for that label)."""
+    cce_norm_forward(X, norm_w, eps, H8=buf.H8, Hs=buf.Hs, stream=stream)
+    cce_fp8_matmul(buf.H8, buf.Hs, head.q, head.s, buf.logits, buf.ws, stream)
+    cce_sample_rows(buf.logits, temperature, top_k, top_p, min_p, u, buf.tokens, buf.logp, stream)

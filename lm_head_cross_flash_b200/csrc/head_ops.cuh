@@ -80,12 +80,13 @@ void with_team(int64_t D, F f) {
   f(Int<512>(), Int<4>());
 }
 
-// Blocks of the norm's backward: enough to fill the SMs, each with several
-// rows where there are many, so that the parts of dw stay a small share.
-int norm_bwd_blocks(int64_t M, int64_t D) {
-  int rpb = 1;
-  with_team<true>(D, [&](auto tpr, auto) { rpb = norm_block(tpr()) / tpr(); });
-  const int64_t per_sm = D > 256 * 8 ? 2 : 4;
+// Blocks of the norm's kernels: what runs at once.
+int norm_blocks(int64_t M, int64_t D) {
+  int64_t rpb = 1, per_sm = 1;
+  with_team<true>(D, [&](auto tpr, auto r) {
+    rpb = norm_block(tpr()) / tpr();
+    per_sm = norm_per_sm(tpr(), r());
+  });
   return int(std::max<int64_t>(1, std::min<int64_t>(ceil_div(M, rpb), per_sm * sm_count_guess())));
 }
 
@@ -210,15 +211,22 @@ cce_status cce_fp8_quant_rows(const void* X, cce_dtype x_dtype, int64_t M, int64
   if (s != CCE_OK) return s;
   if (D > kMaxQuantD) return CCE_ERR_UNSUPPORTED;
   const int G = int(ceil_div(D, QGROUP));
-  const int grid = int(std::min<int64_t>(ceil_div(M * G, 16), 16 * sm_count_guess()));
+  const bool vec = D % 8 == 0 && rows16(X, ldx, dtype_bytes(x_dtype)) && codes8(Q, ldq);
+  // Four groups of a half warp under way where every SM still gets four blocks
+  // ([16384, 4096] bf16: 41 us, 47 with one; [250, 4096]: 2.9 us, 2.4 with one).
+  const int sms = sm_count_guess();
+  const bool many = M * G >= int64_t(4) * sms * 64;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(PK_QUANT, st);
-  const bool vec = D % 8 == 0 && rows16(X, ldx, dtype_bytes(x_dtype)) && codes8(Q, ldq);
   with_type(x_dtype, [&](auto t) {
     using T = typename decltype(t)::type;
     with_bool(vec, [&](auto v) {
-      quant_rows_kernel<decltype(v)::value, T><<<grid, 256, 0, st>>>(
-          static_cast<const T*>(X), ldx, M, int(D), G, qmat(Q, ldq, S, D));
+      with_bool(many, [&](auto m) {
+        constexpr int UN = decltype(m)::value ? 4 : 1;
+        const int grid = int(std::min<int64_t>(ceil_div(M * G, 16 * UN), 16 * sms));
+        quant_rows_kernel<decltype(v)::value, T, UN><<<grid, 256, 0, st>>>(
+            static_cast<const T*>(X), ldx, M, int(D), G, qmat(Q, ldq, S, D));
+      });
     });
   });
   return launch_ok();
@@ -268,6 +276,7 @@ cce_status cce_norm_forward(const void* X, cce_dtype x_dtype, int64_t M, int64_t
   a.w_bf16 = w_dtype == CCE_BF16;
   a.M = M;
   a.D = int(D);
+  a.inv_d = float(1.0 / double(D));
   a.eps = float(eps);
   a.h = H;
   a.ldh = ldh;
@@ -284,10 +293,9 @@ cce_status cce_norm_forward(const void* X, cce_dtype x_dtype, int64_t M, int64_t
       with_bool(vec, [&](auto v) {
         with_team<decltype(v)::value>(D, [&](auto tpr, auto r) {
           constexpr int T = decltype(tpr)::value, B = norm_block(T);
-          const int grid = int(std::min<int64_t>(ceil_div(M, B / T), 32 * sm_count_guess()));
           norm_fwd_kernel<decltype(v)::value, typename decltype(tx)::type,
                           typename decltype(th)::type, T, decltype(r)::value>
-              <<<grid, B, 0, st>>>(a);
+              <<<norm_blocks(M, D), B, 0, st>>>(a);
         });
       });
     });
@@ -297,7 +305,7 @@ cce_status cce_norm_forward(const void* X, cce_dtype x_dtype, int64_t M, int64_t
 
 size_t cce_norm_backward_workspace_bytes(int64_t M, int64_t D) {
   if (M <= 0 || D <= 0 || M > kMaxRows || D > kMaxNormD) return 0;
-  return kStatusBytes + size_t(norm_bwd_blocks(M, D)) * size_t(D) * 4;
+  return kStatusBytes + size_t(norm_blocks(M, D)) * size_t(D) * 4;
 }
 
 cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs, const float* rstd,
@@ -326,6 +334,7 @@ cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs, c
   a.lddh = lddh;
   a.M = M;
   a.D = int(D);
+  a.inv_d = float(1.0 / double(D));
   a.dx = dX;
   a.lddx = lddx;
   const bool vec = D % 8 == 0 && rows16(dH, lddh, dtype_bytes(dh_dtype)) &&
@@ -333,7 +342,7 @@ cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs, c
                    codes8(X8, ldx8);
   if (dW != nullptr)
     a.dw_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
-  const int grid = norm_bwd_blocks(M, D);
+  const int grid = norm_blocks(M, D);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(PK_NORM, st);
   with_type(dx_dtype, [&](auto tx) {
@@ -350,7 +359,7 @@ cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs, c
   });
   if (launch_ok() != CCE_OK) return CCE_ERR_CUDA;
   if (dW != nullptr)
-    norm_dw_kernel<<<unsigned(ceil_div(D, 32)), 256, 0, st>>>(a.dw_part, grid, int(D), dW);
+    norm_dw_kernel<<<unsigned(ceil_div(D, 32)), 1024, 0, st>>>(a.dw_part, grid, int(D), dW);
   return launch_ok();
 }
 

@@ -6,7 +6,7 @@
 // Format.  A group holds e4m3 codes q and one fp32 scale s; its values are
 // q * s.  With m = max(|x|) over the group, at least 2^-90 so that nothing
 // below leaves the fp32 range,
-//   s = m / 448,  q = e4m3(x * (448 * (1 / m))),
+//   s = m * (1 / 448),  q = e4m3(x * (448 * (1 / m))),
 // the quotients and the products rounded in fp32, the code rounded to nearest
 // even and saturated.  e4m3 keeps the relative error of every element above
 // m * 2^-15 within 2^-4, where an 8-bit integer would lose the small elements
@@ -25,6 +25,7 @@ namespace cce {
 
 constexpr int QGROUP = 128;
 constexpr float E4M3_MAX = 448.f;
+constexpr float E4M3_INV = 1.f / 448.f;
 constexpr float QAMAX_MIN = 8.077935669463161e-28f;  // 2^-90
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -61,6 +62,49 @@ __device__ __forceinline__ void load8(const T* __restrict__ p, int c, int n, flo
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c + i < n ? to_f32(p[c + i]) : 0.f;
+  }
+}
+
+// The same eight elements as they lie in memory, for loads that run ahead.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <bool VEC, typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* __restrict__ p, int c, int n) {
+  Raw8<T> r;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i)
+      r.v[i] = __ldg(reinterpret_cast<const uint4*>(p + c) + i);
+  } else {
+    uint32_t w[2 * sizeof(T)] = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) {
+        if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(p[c + i]);
+        else w[i / 2] |= uint32_t(__bfloat16_as_ushort(p[c + i])) << (16 * (i & 1));
+      }
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i)
+      r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void open8(const Raw8<T>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < int(sizeof(T) / 2); ++i) {
+    const uint32_t u[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        v[4 * i + j] = __uint_as_float(u[j]);
+      } else {
+        v[2 * j] = __uint_as_float(u[j] << 16);
+        v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+      }
+    }
   }
 }
 
@@ -158,7 +202,7 @@ struct QMat {
 };
 
 __device__ __forceinline__ float code_factor(float m) {
-  return __fmul_rn(E4M3_MAX, __fdiv_rn(1.f, m));
+  return __fmul_rn(E4M3_MAX, __frcp_rn(m));
 }
 
 // Codes and scale of the group that the 16 lanes of this half warp hold.
@@ -168,26 +212,38 @@ __device__ __forceinline__ void quant_group(const QMat& o, int64_t row, int c, i
   const float m = group_max(amax8(v));
   if (c < n) {
     store_codes8<VEC>(o.q + row * o.ldq, c, n, codes8(v, code_factor(m)));
-    if ((c & (QGROUP - 1)) == 0) o.s[row * o.lds + c / QGROUP] = __fdiv_rn(m, E4M3_MAX);
+    if ((c & (QGROUP - 1)) == 0) o.s[row * o.lds + c / QGROUP] = __fmul_rn(m, E4M3_INV);
   }
 }
 
 // ------------------------------------------------------------ quant rows --
-// A half warp takes one group: 16 lanes x 8 elements.  Reads each element
-// once; bound by bandwidth.
-template <bool VEC, typename T>
+// A half warp takes one group: 16 lanes x 8 elements, UN groups under way at
+// once.  Reads each element once; bound by bandwidth.
+template <bool VEC, typename T, int UN>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x, int64_t ldx,
                                                          int64_t M, int D, int G, QMat o) {
   const int64_t n = M * G;
-  const int64_t step = int64_t(gridDim.x) * 16;
+  const int lane8 = (threadIdx.x & 15) * 8;
   // whole warps stay together: group_max shuffles over the full warp
-  for (int64_t u0 = int64_t(blockIdx.x) * 16 + (threadIdx.x >> 5) * 2; u0 < n; u0 += step) {
-    const int64_t u = u0 + ((threadIdx.x >> 4) & 1);
-    const int64_t row = u / G;
-    const int c = u < n ? int(u - row * G) * QGROUP + (threadIdx.x & 15) * 8 : D;
-    float v[8] = {};
-    if (c < D) load8<VEC>(x + row * ldx, c, D, v);
-    quant_group<VEC>(o, row, c, D, v);
+  for (int64_t u0 = int64_t(blockIdx.x) * (16 * UN) + (threadIdx.x >> 5) * 2; u0 < n;
+       u0 += int64_t(gridDim.x) * (16 * UN)) {
+    Raw8<T> r[UN];
+    int64_t row[UN];
+    int c[UN];
+#pragma unroll
+    for (int k = 0; k < UN; ++k) {
+      const int64_t u = u0 + 16 * k + ((threadIdx.x >> 4) & 1);
+      row[k] = u / G;
+      c[k] = u < n ? int(u - row[k] * G) * QGROUP + lane8 : D;
+      r[k] = Raw8<T>();
+      if (c[k] < D) r[k] = raw8<VEC>(x + row[k] * ldx, c[k], D);
+    }
+#pragma unroll
+    for (int k = 0; k < UN; ++k) {
+      float v[8];
+      open8<T>(r[k], v);
+      quant_group<VEC>(o, row[k], c[k], D, v);
+    }
   }
 }
 
@@ -224,23 +280,23 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const T* __restrict__
     const int64_t row = row0 + 16 * i;
     if (row < N && c < K) store_codes8<VEC>(o.q + row * o.ldq, c, K, codes8(v[i], inv));
   }
-  if (threadIdx.x == 0) o.s[blockIdx.y * o.lds + g] = __fdiv_rn(m, E4M3_MAX);
+  if (threadIdx.x == 0) o.s[blockIdx.y * o.lds + g] = __fmul_rn(m, E4M3_INV);
 }
 
 // ------------------------------------------------------------------ norm --
 // Sum over the TPR threads of one row; every thread of the block calls it.
-template <int TPR>
-__device__ __forceinline__ float team_sum(float s, float* sm) {
+// Two buffers taken in turn, so one barrier a sum is enough.
+template <int TPR, int WARPS>
+__device__ __forceinline__ float team_sum(float s, float (&sm)[2][WARPS], int turn) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   if constexpr (TPR > 32) {
     const int warp = threadIdx.x >> 5, w0 = warp & ~(TPR / 32 - 1);
-    __syncthreads();  // the last sum has been read
-    if ((threadIdx.x & 31) == 0) sm[warp] = s;
+    if ((threadIdx.x & 31) == 0) sm[turn & 1][warp] = s;
     __syncthreads();
-    s = 0.f;
+    s = sm[turn & 1][w0 + (threadIdx.x & (TPR / 32 - 1))];
 #pragma unroll
-    for (int i = 0; i < TPR / 32; ++i) s += sm[w0 + i];
+    for (int off = TPR / 64; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
   }
   return s;
 }
@@ -252,7 +308,7 @@ struct NormFwdArgs {
   int w_bf16;
   int64_t M;
   int D;
-  float eps;
+  float inv_d, eps;
   void* h;       // null: not wanted
   int64_t ldh;
   QMat h8, x8;   // q null: not wanted
@@ -266,32 +322,55 @@ __device__ __forceinline__ void load_w8(const void* w, int bf16, int c, int n, f
 }
 
 constexpr int norm_block(int tpr) { return tpr > 256 ? tpr : 256; }
+// Blocks that share an SM where a thread has one piece of the row: 1,024
+// threads of 64 registers, or 768 of 80 where the block's teams also meet.
+constexpr int norm_per_sm(int tpr, int r) {
+  return r > 1 ? 1 : tpr < 256 ? 3 : 1024 / norm_block(tpr);
+}
 
 // h = x * rstd * w with rstd = 1 / sqrt(mean(x^2) + eps), all in fp32.  TPR
 // threads hold a row in registers (R pieces of 8 elements each), so x is read
-// once; the codes of x and of h come from the same registers.
+// once; the codes of x and of h come from the same registers.  A block takes
+// row after row, the next one on its way while the current one is summed.
 template <bool VEC, typename T, typename TH, int TPR, int R>
-__global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormFwdArgs a) {
+__global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR, R))
+    norm_fwd_kernel(const __grid_constant__ NormFwdArgs a) {
   constexpr int RPB = norm_block(TPR) / TPR;
-  __shared__ float sm[norm_block(TPR) / 32];
+  __shared__ float sm[2][norm_block(TPR) / 32];
   const int t = threadIdx.x % TPR;
-  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.M; row0 += int64_t(gridDim.x) * RPB) {
-    const int64_t row = row0 + threadIdx.x / TPR;
-    const bool live = row < a.M;
-    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
-    float v[R][8] = {};
-    float ss = 0.f;
+  // One piece a thread: the weights stay in registers too.
+  constexpr bool KEEP = R == 1;
+  float w[R][8];
+  if constexpr (KEEP) {
+    if (t * 8 < a.D) load_w8<VEC>(a.w, a.w_bf16, t * 8, a.D, w[0]);
+  }
+  Raw8<T> x[R];
+  const int64_t step = int64_t(gridDim.x) * RPB;
+  int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
+  const T* src = static_cast<const T*>(a.x) + row * a.ldx;  // of the next fetch
+  auto fetch = [&](bool live) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int c = (i * TPR + t) * 8;
-      if (live && c < a.D) load8<VEC>(x, c, a.D, v[i]);
+      x[i] = Raw8<T>();
+      if (live && c < a.D) x[i] = raw8<VEC>(src, c, a.D);
     }
+    src += step * a.ldx;
+  };
+  fetch(row < a.M);
+  int turn = 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.M; row0 += step, row += step, ++turn) {
+    const bool live = row < a.M;
+    float v[R][8], ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
+      open8<T>(x[i], v[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-    ss = team_sum<TPR>(ss, sm);
-    const float rstd = __fdiv_rn(1.f, __fsqrt_rn(ss / float(a.D) + a.eps));
+    }
+    fetch(row + step < a.M);
+    ss = team_sum<TPR>(ss, sm, turn);
+    const float rstd = rsqrtf(fmaf(ss, a.inv_d, a.eps));
     if (live && t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -301,9 +380,9 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormFwdArgs a
       if (a.h == nullptr && a.h8.q == nullptr) continue;
       float h[8] = {};
       if (cl < a.D) {
-        load_w8<VEC>(a.w, a.w_bf16, c, a.D, h);
+        if constexpr (!KEEP) load_w8<VEC>(a.w, a.w_bf16, c, a.D, w[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] *= v[i][j] * rstd;
+        for (int j = 0; j < 8; ++j) h[j] = v[i][j] * rstd * w[i][j];
         if (a.h != nullptr) store8<VEC>(static_cast<TH*>(a.h) + row * a.ldh, c, a.D, h);
       }
       if (a.h8.q != nullptr) quant_group<VEC>(a.h8, row, cl, a.D, h);
@@ -320,6 +399,7 @@ struct NormBwdArgs {
   int64_t lddh;
   int64_t M;
   int D;
+  float inv_d;
   void* dx;
   int64_t lddx;
   float* dw_part;  // [gridDim.x, D] or null
@@ -334,9 +414,10 @@ struct NormBwdArgs {
 // norm_dw_kernel, so dw does not depend on timing.
 // The next row's loads are issued before the current row's sum.
 template <bool VEC, typename TX, typename TH, int TPR, int R>
-__global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormBwdArgs a) {
+__global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR, R))
+    norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {
   constexpr int RPB = norm_block(TPR) / TPR;
-  __shared__ float sm[norm_block(TPR) / 32];
+  __shared__ float sm[2][norm_block(TPR) / 32];
   __shared__ float sw[RPB > 1 ? (RPB - 1) * TPR * R * 8 : 1];
   const int t = threadIdx.x % TPR;
   float w[R][8], dw[R][8] = {};
@@ -349,7 +430,8 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormBwdArgs a
   }
   // one row as it comes from memory
   uint2 q[R];
-  float g[R][8], sc[R], rstd;
+  Raw8<TH> dh[R];
+  float sc[R], rstd;
   auto fetch = [&](int64_t row) {
     const bool live = row < a.M;
     rstd = live ? __ldg(a.rstd + row) : 0.f;
@@ -358,11 +440,10 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormBwdArgs a
       const int c = (i * TPR + t) * 8;
       q[i] = make_uint2(0, 0);
       sc[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[i][j] = 0.f;
+      dh[i] = Raw8<TH>();
       if (live && c < a.D) {
         q[i] = load_codes8<VEC>(a.x8.q + row * a.x8.ldq, c, a.D);
-        load8<VEC>(static_cast<const TH*>(a.dh) + row * a.lddh, c, a.D, g[i]);
+        dh[i] = raw8<VEC>(static_cast<const TH*>(a.dh) + row * a.lddh, c, a.D);
         sc[i] = __ldg(a.x8.s + row * a.x8.lds + c / QGROUP);
       }
     }
@@ -370,24 +451,27 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormBwdArgs a
   const int64_t step = int64_t(gridDim.x) * RPB;
   int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
   fetch(row);
-  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.M; row0 += step, row += step) {
+  int turn = 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.M; row0 += step, row += step, ++turn) {
     float n[R][8], h[R][8];
     const float r = rstd;
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float k = sc[i] * r;
+      float g[8];
       code_values8(q[i], n[i]);
+      open8<TH>(dh[i], g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         n[i][j] *= k;
-        dw[i][j] = fmaf(g[i][j], n[i][j], dw[i][j]);
-        h[i][j] = g[i][j] * w[i][j];
+        dw[i][j] = fmaf(g[j], n[i][j], dw[i][j]);
+        h[i][j] = g[j] * w[i][j];
         dot = fmaf(h[i][j], n[i][j], dot);
       }
     }
     fetch(row + step);
-    dot = team_sum<TPR>(dot, sm) / float(a.D);
+    dot = team_sum<TPR>(dot, sm, turn) * a.inv_d;
     if (row < a.M) {
 #pragma unroll
       for (int i = 0; i < R; ++i) {
@@ -425,20 +509,28 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormBwdArgs a
   }
 }
 
-// dw[d] = sum over p of part[p, d]: 32 columns a block, 8 slices of the parts
+// dw[d] = sum over p of part[p, d]: 32 columns a block, 32 slices of the parts
 // a column, each in order, then the slices in order.
-__global__ void __launch_bounds__(256) norm_dw_kernel(const float* __restrict__ part, int P, int D,
-                                                      float* __restrict__ dw) {
-  __shared__ float sm[8][33];
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__ part, int P, int D,
+                                                       float* __restrict__ dw) {
+  __shared__ float sm[32][33];
   const int d = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
   float s = 0.f;
-  if (d < D)
-    for (int p = k; p < P; p += 8) s += __ldg(part + size_t(p) * D + d);
+  if (d < D) {
+    int p = k;
+    for (; p + 96 < P; p += 128) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __ldg(part + size_t(p + 32 * i) * D + d);
+      s += (v[0] + v[1]) + (v[2] + v[3]);
+    }
+    for (; p < P; p += 32) s += __ldg(part + size_t(p) * D + d);
+  }
   sm[k][threadIdx.x & 31] = s;
   __syncthreads();
   if (k == 0 && d < D) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += sm[i][threadIdx.x];
+    for (int i = 1; i < 32; ++i) s += sm[i][threadIdx.x];
     dw[d] = s;
   }
 }

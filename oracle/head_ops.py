@@ -30,7 +30,7 @@ def _codes(x, m):
     products rounded in fp32 as the format defines them."""
     with np.errstate(all="ignore"):
         inv = np.float32(448.0) * (np.float32(1.0) / m)
-        return e4m3_round((x * inv).astype(np.float32)), m / np.float32(448.0)
+        return e4m3_round((x * inv).astype(np.float32)), m * (np.float32(1.0) / np.float32(448.0))
 
 
 def _amax(x, axis):
