@@ -161,7 +161,7 @@ cce_status launch_sample(SampleArgs a, int64_t B, int c, cudaStream_t st) {
   static bool done[64];
   const cce_status s = set_smem_once(sample_kernel<T, MODE>, int(sizeof(SaShared)), done);
   if (s != CCE_OK) return s;
-  a.slice = int(ceil_div(ceil_div(a.V, c), SA_SEG)) * SA_SEG;
+  a.slice = int(ceil_div(ceil_div(int64_t(a.V) + 7, c), SA_SEG)) * SA_SEG;  // + off_
   a.seg_mul = int(ceil_div(a.slice / SA_SEG, SA_MAX_SEGS));
   cudaLaunchConfig_t cfg = {};
   // the search: as many clusters as run at once (one CTA on an SM)
@@ -465,7 +465,6 @@ cce_status cce_sample_rows(const void* logits, cce_dtype dtype, int64_t B, int64
   a.ld = ld;
   a.B = int(B);
   a.V = int(V);
-  a.vec = rows16(logits, ld, dtype_bytes(dtype));
   int log2v = 0;
   while ((int64_t(1) << log2v) < V) ++log2v;
   a.bits = std::min(45, 63 - log2v);  // a row's mass stays below 2^63

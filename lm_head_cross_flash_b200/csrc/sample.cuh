@@ -68,7 +68,6 @@ struct SampleArgs {
   int B, V;
   int slice;    // logits per CTA, a multiple of SA_SEG
   int seg_mul;  // segments that share an entry of segs[]
-  int vec;      // rows start on 16-byte boundaries
   int bits;     // binary places of a weight
   const float* temperature;  // the next four may be null: 1, off, off, off
   const int32_t* top_k;
@@ -168,8 +167,9 @@ class Sampler {
     me_ = int(cl_.block_rank());
     row_ = row;
     g_ = static_cast<const T*>(a.logits) + int64_t(row_) * a.ld;
-    s0_ = int(min(int64_t(a.V), int64_t(me_) * a.slice));
-    s1_ = int(min(int64_t(a.V), int64_t(s0_) + a.slice));
+    off_ = int((reinterpret_cast<uintptr_t>(g_) & 15) / sizeof(T));
+    s0_ = int(min(int64_t(a.V) + off_, int64_t(me_) * a.slice));
+    s1_ = int(min(int64_t(a.V) + off_, int64_t(s0_) + a.slice));
   }
 
   template <int MODE>
@@ -179,7 +179,10 @@ class Sampler {
   const SampleArgs& a_;
   SaShared& s_;
   cooperative_groups::cluster_group cl_;
-  int C_, me_, row_, s0_, s1_;
+  // Positions count from the 16-byte boundary at or before the row's first
+  // logit, off_ logits ahead of it, so that pieces of eight are whole 16-byte
+  // loads wherever the row begins.  The slice is [s0_, s1_).
+  int C_, me_, row_, off_, s0_, s1_;
   const T* g_;
   int turn_ = 0;      // which half of `parts` the next exchange uses
   float max_ = 0.f;
@@ -189,24 +192,25 @@ class Sampler {
 
   // ------------------------------------------------------------- passes --
   __device__ SaRaw<T> fetch(int c) const {
-    if (!a_.vec || c + 8 > s1_) return fetch_ragged(g_, c, s1_);
+    if (c < off_ || c + 8 > s1_) return fetch_ragged(g_, c - off_, s1_ - off_);
     SaRaw<T> r;
 #pragma unroll
     for (int i = 0; i < int(sizeof(T) / 2); ++i)
-      r.v[i] = __ldg(reinterpret_cast<const uint4*>(g_ + c) + i);
+      r.v[i] = __ldg(reinterpret_cast<const uint4*>(g_ - off_ + c) + i);
     return r;
   }
-  // -inf behind the end
+  // From index c on, -inf outside [0, end).
   __device__ static __noinline__ SaRaw<T> fetch_ragged(const T* g, int c, int end) {
+    auto in = [&](int i) { return i >= 0 && i < end; };
     SaRaw<T> r;
     uint32_t w[sizeof(T) * 2];
 #pragma unroll
     for (int i = 0; i < int(sizeof(T) * 2); ++i) {
       if constexpr (sizeof(T) == 4) {
-        w[i] = c + i < end ? __float_as_uint(g[c + i]) : 0xFF800000u;
+        w[i] = in(c + i) ? __float_as_uint(g[c + i]) : 0xFF800000u;
       } else {
-        const uint32_t lo = c + 2 * i < end ? __bfloat16_as_ushort(g[c + 2 * i]) : 0xFF80u;
-        const uint32_t hi = c + 2 * i + 1 < end ? __bfloat16_as_ushort(g[c + 2 * i + 1]) : 0xFF80u;
+        const uint32_t lo = in(c + 2 * i) ? __bfloat16_as_ushort(g[c + 2 * i]) : 0xFF80u;
+        const uint32_t hi = in(c + 2 * i + 1) ? __bfloat16_as_ushort(g[c + 2 * i + 1]) : 0xFF80u;
         w[i] = lo | (hi << 16);
       }
     }
@@ -247,7 +251,7 @@ class Sampler {
       if (i < to) ahead = fetch(next);
       float v[8];
       raw_values<T>(r, v);
-      f(v, c);
+      f(v, c - off_);
       c = next;
       r = ahead;
     }
@@ -562,9 +566,18 @@ class Sampler {
   __device__ static u64 nucleus(float tp, double z) {  // ceil(tp z), one at least
     return u64(fmax(1.0, ceil(double(tp) * z)));
   }
+  // What is known of the mass of all live logits.
+  struct Total {
+    bool exact;
+    u64 mass;       // if exact
+    double lo, hi;  // if not
+  };
   // Both set res_rank to the chosen rank; by_list returns false if it cannot
   // be sure of it.
   __device__ bool by_list(const Settings& o, const SaFirst& f);
+  // From the list, which holds a prefix of the ranks (all: every one), if that
+  // is sure to hold what stays; a barrier of the cluster on both sides.
+  __device__ bool finish(const Settings& o, const Total& z, bool all);
   __device__ void by_search(const Settings& o);
   // The rank at which the running count (by_mass: mass) reaches the target
   // (at least 1, at most the total): res_rank, and by mass res_cum.
@@ -708,13 +721,13 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
   static_assert(DEPTH >= 2 && (DEPTH & (DEPTH - 1)) == 0, "a power of two");
   const int cw = s0_ + warp * SA_SEG;  // where the warp's first segment begins
   const int np = cw < s1_ ? (s1_ - cw + STEP - 1) / STEP : 0;
-  const int full = a_.vec && s1_ - cw >= SA_SEG ? (s1_ - cw - SA_SEG) / STEP + 1 : 0;
+  const int full = s1_ - cw >= SA_SEG ? (s1_ - cw - SA_SEG) / STEP + 1 : 0;
   uint4* const ring = reinterpret_cast<uint4*>(s_.ring) + threadIdx.x;
   auto slot = [&](int p) { return ring + (p & (DEPTH - 1)) * (NB * PL * SA_THREADS); };
   auto issue = [&](int p) {
-    if (p < full) {
+    if (p < full && (p > 0 || cw >= off_)) {
       const uint32_t to = smem_u32(slot(p));
-      const uint4* from = reinterpret_cast<const uint4*>(g_ + cw + p * STEP + lane * 8);
+      const uint4* from = reinterpret_cast<const uint4*>(g_ - off_ + cw + p * STEP + lane * 8);
 #pragma unroll
       for (int i = 0; i < NB * PL; ++i)
         asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
@@ -792,7 +805,7 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
           const float l = v[k][j];
           if (l == m) {
             ++ne;
-            mi = min(mi, cw + p * STEP + k * 256 + lane * 8 + j);
+            mi = min(mi, cw + p * STEP + k * 256 + lane * 8 + j - off_);
           } else if (l - m > -INFINITY) {
             const float x = fmaf(l, CT, -ht), y = fmaf(l, cz, -hz);
             sum_t += ex2_approx(x);
@@ -929,10 +942,21 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
       if (c[k] >= s1_) continue;
       float v[8];
       raw_values<T>(r[k], v);
-      each_hit(v, c[k], [&](float l, int) { return bin_below(max_, l, scale) <= last; },
+      each_hit(v, c[k] - off_, [&](float l, int) { return bin_below(max_, l, scale) <= last; },
                [&](u64 q) { append(q); });
     }
   }
+  const double unit = double(u64(1) << a_.bits);
+  Total z;
+  z.exact = all;
+  z.mass = 0;
+  z.lo = (double(f.n) + f.z * (1.0 - SA_SUM_ERROR)) * unit - double(a_.V);
+  z.hi = (double(f.n) + f.z * (1.0 + SA_SUM_ERROR)) * unit + double(a_.V);
+  return finish(o, z, all);
+}
+
+template <typename T>
+__device__ bool Sampler<T>::finish(const Settings& o, const Total& z, bool all) {
   cl_.sync();
   if (me_ == 0) {
     bool ok = s_.n_list <= SA_CAP;
@@ -948,20 +972,13 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
       }
       __syncthreads();
       const u64 end = s_.end;
-      // mass of the kept ranks: exact (lo = hi), or the total from the pass
-      double lo, hi;
-      u64 keep = 0;
-      bool exact = true;
+      // mass of the kept ranks: exact, or between two bounds
+      u64 keep = all ? end : z.mass;
+      bool exact = z.exact;
       if (o.k > 0) {
         ok = all || n >= o.k;
         keep = s_.res_cum;
-      } else if (all) {
-        keep = end;
-      } else {
-        exact = false;
-        const double unit = double(u64(1) << a_.bits);
-        lo = (double(f.n) + f.z * (1.0 - SA_SUM_ERROR)) * unit - double(a_.V);
-        hi = (double(f.n) + f.z * (1.0 + SA_SUM_ERROR)) * unit + double(a_.V);
+        exact = true;
       }
       // the rank that both ends of the interval lead to
       auto settle = [&](u64 a, u64 b) {
@@ -972,7 +989,7 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
       };
       if (ok && o.use_p) {
         ok = exact ? settle(min(nucleus(o.tp, double(keep)), keep), min(nucleus(o.tp, double(keep)), keep))
-                   : settle(nucleus(o.tp, lo), nucleus(o.tp, hi));
+                   : settle(nucleus(o.tp, z.lo), nucleus(o.tp, z.hi));
         keep = exact ? min(keep, s_.res_cum) : s_.res_cum;
         exact = true;
       }
@@ -990,7 +1007,7 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
       }
       if (ok)
         ok = exact ? settle(part_of(o.u, double(keep)) + 1, part_of(o.u, double(keep)) + 1)
-                   : settle(part_of(o.u, lo) + 1, part_of(o.u, hi) + 1);
+                   : settle(part_of(o.u, z.lo) + 1, part_of(o.u, z.hi) + 1);
     }
     __syncthreads();
     if (threadIdx.x == 0) s_.n_list = 0;  // it may have run over
@@ -1021,8 +1038,35 @@ __device__ void Sampler<T>::by_search(const Settings& o) {
   __syncthreads();
   live = s_.base;
   keep = s_.end;
-  if (o.k > 0 && u64(o.k) < live) {
-    find(false, u64(o.k));
+  // The bin that the first filter, or the draw, ends in.  If all ranks down to
+  // it fit a list, that settles the rest.
+  Settings p = o;
+  if (u64(o.k) >= live) p.k = 0;
+  if (p.k > 0) locate(false, u64(p.k));
+  else if (p.use_p) locate(true, min(nucleus(p.tp, double(keep)), keep));
+  else if (!p.use_m) locate(true, part_of(p.u, double(keep)) + 1);
+  const int last = p.k > 0 || p.use_p || !p.use_m
+                       ? s_.bin
+                       : int(fmin(floor(-p.thr * (1.0 + 0x1p-20) * double(bin_scale_)) + 1.0,
+                                  double(SA_BINS - 1)));
+  u64 n = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (int(threadIdx.x) * 4 + i <= last) n += s_.tot[threadIdx.x * 4 + i];
+  __syncthreads();
+  n = scan(n, s_.warp_sum[0]);
+  if (threadIdx.x == SA_THREADS - 1) s_.base = n;
+  __syncthreads();
+  if (s_.base <= SA_CAP) {
+    pass(
+        0, n_segs(), [&](uint32_t key) { return bin_of(key_value(key)) <= last; },
+        [&](const float (&v)[8], int c) {
+          each_hit(v, c, [&](float l, int) { return bin_of(l) <= last; }, [&](u64 r) { append(r); });
+        });
+    if (finish(p, Total{true, keep, 0.0, 0.0}, false)) return;
+  }
+  if (p.k > 0) {
+    find(false, u64(p.k));
     const u64 cut = s_.res_rank;
     keep = mass_of([&](float l, int i) { return rank_of(l, i) >= cut; });
   }
