@@ -183,14 +183,14 @@ cce_status launch_sample(SampleArgs a, int64_t B, int c, cudaStream_t st) {
              : (cudaGetLastError(), CCE_ERR_CUDA);
 }
 
-// One launch where every row gets as many CTAs as it can use, else two (256
+// One launch where a row gets nearly as many CTAs as it can use, else two (256
 // rows of 262,144 bf16 logits with top-k 50: 67 us with one CTA a row, 165 us
 // with eight).
 template <typename T>
 cce_status launch_sample_rows(const SampleArgs& a, int64_t B, cudaStream_t st) {
   const int c = sample_cluster(B, a.V, sm_count_guess());
   const int most = sample_cluster(1, a.V, sm_count_guess());
-  if (c == most) return launch_sample<T, SA_BOTH>(a, B, c, st);
+  if (2 * c >= most) return launch_sample<T, SA_BOTH>(a, B, c, st);
   const cce_status s = launch_sample<T, SA_LIST_ONLY>(a, B, c, st);
   // Fewer CTAs a row where many rows may be left: 256 rows of 262,144 bf16
   // logits, all of them flat, take 627 us with 2, 782 with 4, 1134 with 8; but

@@ -578,7 +578,7 @@ class Sampler {
   // From the list, which holds a prefix of the ranks (all: every one), if that
   // is sure to hold what stays; a barrier of the cluster on both sides.
   __device__ bool finish(const Settings& o, const Total& z, bool all);
-  __device__ void by_search(const Settings& o);
+  __device__ void by_search(const Settings& o, const SaFirst& f);
   // The rank at which the running count (by_mass: mass) reaches the target
   // (at least 1, at most the total): res_rank, and by mass res_cum.
   // Not inlined (three calls): works on a copy, so that the members stay in
@@ -1018,7 +1018,37 @@ __device__ bool Sampler<T>::finish(const Settings& o, const Total& z, bool all) 
 }
 
 template <typename T>
-__device__ void Sampler<T>::by_search(const Settings& o) {
+__device__ void Sampler<T>::by_search(const Settings& o, const SaFirst& f) {
+  // Whether all ranks down to `last`, in bins of this scale, fit a list, and
+  // settle the rest.
+  auto settled = [&](const Settings& p, int last, float scale, u64 keep) {
+    u64 n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (int(threadIdx.x) * 4 + i <= last) n += s_.tot[threadIdx.x * 4 + i];
+    __syncthreads();
+    n = scan(n, s_.warp_sum[0]);
+    if (threadIdx.x == SA_THREADS - 1) s_.base = n;
+    __syncthreads();
+    if (s_.base > SA_CAP) return false;
+    pass(
+        0, n_segs(), [&](uint32_t key) { return bin_below(max_, key_value(key), scale) <= last; },
+        [&](const float (&v)[8], int c) {
+          each_hit(v, c, [&](float l, int) { return bin_below(max_, l, scale) <= last; },
+                   [&](u64 r) { append(r); });
+        });
+    return finish(p, Total{true, keep, 0.0, 0.0}, false);
+  };
+  if (o.k > 0 && o.k <= SA_CAP) {
+    // Counts alone, down to twice as far as the least of the segments' maxima.
+    const float scale = scale_for(2.f * below(f.least));
+    bin_up(false, [](uint32_t) { return true; },
+           [&](float l, int) { return bin_below(max_, l, scale); });
+    locate(false, u64(o.k));
+    const int last = s_.bin;
+    if (s_.base + s_.n_in >= u64(o.k) && settled(o, last, scale, 0)) return;
+    cl_.sync();  // the counts have been read
+  }
   // Bins over 24 T: what lies below has less than 4e-11 of the largest weight
   // each, and falls into the last bin.
   bin_scale_ = scale_for(24.f * o.temp);
@@ -1038,37 +1068,21 @@ __device__ void Sampler<T>::by_search(const Settings& o) {
   __syncthreads();
   live = s_.base;
   keep = s_.end;
-  // The bin that the first filter, or the draw, ends in.  If all ranks down to
-  // it fit a list, that settles the rest.
   Settings p = o;
   if (u64(o.k) >= live) p.k = 0;
-  if (p.k > 0) locate(false, u64(p.k));
-  else if (p.use_p) locate(true, min(nucleus(p.tp, double(keep)), keep));
-  else if (!p.use_m) locate(true, part_of(p.u, double(keep)) + 1);
-  const int last = p.k > 0 || p.use_p || !p.use_m
-                       ? s_.bin
-                       : int(fmin(floor(-p.thr * (1.0 + 0x1p-20) * double(bin_scale_)) + 1.0,
-                                  double(SA_BINS - 1)));
-  u64 n = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (int(threadIdx.x) * 4 + i <= last) n += s_.tot[threadIdx.x * 4 + i];
-  __syncthreads();
-  n = scan(n, s_.warp_sum[0]);
-  if (threadIdx.x == SA_THREADS - 1) s_.base = n;
-  __syncthreads();
-  if (s_.base <= SA_CAP) {
-    pass(
-        0, n_segs(), [&](uint32_t key) { return bin_of(key_value(key)) <= last; },
-        [&](const float (&v)[8], int c) {
-          each_hit(v, c, [&](float l, int) { return bin_of(l) <= last; }, [&](u64 r) { append(r); });
-        });
-    if (finish(p, Total{true, keep, 0.0, 0.0}, false)) return;
-  }
   if (p.k > 0) {
     find(false, u64(p.k));
     const u64 cut = s_.res_rank;
     keep = mass_of([&](float l, int i) { return rank_of(l, i) >= cut; });
+  } else {
+    // the bin that the first filter, or the draw, ends in
+    if (p.use_p) locate(true, min(nucleus(p.tp, double(keep)), keep));
+    else if (!p.use_m) locate(true, part_of(p.u, double(keep)) + 1);
+    const int last = p.use_p || !p.use_m
+                         ? s_.bin
+                         : int(fmin(floor(-p.thr * (1.0 + 0x1p-20) * double(bin_scale_)) + 1.0,
+                                    double(SA_BINS - 1)));
+    if (settled(p, last, bin_scale_, keep)) return;
   }
   if (o.use_p) {
     find(true, min(nucleus(o.tp, double(keep)), keep));
@@ -1123,7 +1137,7 @@ __device__ void Sampler<T>::run() {
         if (lead) a_.token[row_] = SA_UNDECIDED;
         return;
       }
-      by_search(o);
+      by_search(o, f);
     }
     token = s_.res_rank;
   }
