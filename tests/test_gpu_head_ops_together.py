@@ -145,6 +145,45 @@ def test_both_in_graphs():
     assert cce.cce_device_status(a[2].ws) == 0 and cce.cce_device_status(b[2].ws) == 0
 
 
+FIRST_IN_A_CAPTURE = """
+import torch
+from lm_head_cross_flash_b200 import cce
+B, D, V = {B}, 256, 30000
+X, w = torch.randn(B, D, device="cuda"), torch.ones(D, device="cuda")
+W, u = torch.randn(V, D, device="cuda"), torch.full((B,), 0.5, device="cuda")
+q, s = cce.fp8_empty(V, D), torch.empty(cce.fp8_groups(V), cce.fp8_groups(D), device="cuda")
+head = cce.Fp8Head(q, s)
+buf, norm = cce.DecodeBuffers.alloc(B, head), cce.NormBuffers.alloc(B, D, cce.CCE_F32, torch.float32)
+dH = torch.ones(B, D, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    cce.cce_fp8_quant_blocks(W, q, s)
+    cce.decode_step(X, w, 1e-6, head, u, buf, top_p=torch.full((B,), 0.9, device="cuda"))
+    cce.cce_norm_forward(X, w, 1e-6, norm.H, X8=norm.X8, Xs=norm.Xs, rstd=norm.rstd)
+    cce.cce_norm_backward(norm.X8, norm.Xs, norm.rstd, w, dH, norm.dX, norm.dW, norm.ws)
+g.replay()
+torch.cuda.synchronize()
+tokens, dX = buf.tokens.clone(), norm.dX.clone()
+cce.decode_step(X, w, 1e-6, head, u, buf, top_p=torch.full((B,), 0.9, device="cuda"))
+cce.cce_norm_backward(norm.X8, norm.Xs, norm.rstd, w, dH, norm.dX, norm.dW, norm.ws)
+torch.cuda.synchronize()
+assert torch.equal(tokens, buf.tokens) and torch.equal(dX, norm.dX) and (tokens >= 0).all()
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("B", [3, 200])
+def test_the_first_calls_of_a_process_may_be_captured(B):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_A_CAPTURE.replace("{B}", str(B))],
+                       capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
 def test_two_streams_at_once():
     """Two decoding steps on two streams, each with buffers of its own."""
     D, V = 512, 30000

@@ -51,10 +51,12 @@ def f32(*shape):
 
 SHAPES = [(1, 1, 0), (1, 128, 0), (3, 127, 1), (5, 129, 7), (17, 200, 56), (2, 2048, 0),
           (33, 1536, 8), (3, 4096, 0), (2, 8200, 3), (1, 16384, 0)]
+# more rows than run at once: blocks take several
+MANY = [(4001, 200, 0), (3001, 512, 0), (1501, 1000, 24), (700, 4096, 0), (350, 8200, 0), (700, 2047, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("M,D,pad", SHAPES)
+@pytest.mark.parametrize("M,D,pad", SHAPES + [(5001, 1100, 4), (40003, 72, 0)])
 def test_quant_rows_is_exact(M, D, pad, dtype):
     x = rows(1, M, D, dtype, pad)
     q, s = codes(M, D, pad), f32(M, O.groups(D))
@@ -103,7 +105,7 @@ def test_quant_edge_values():
 
 @pytest.mark.parametrize("xt,wt,ht", [("bf16", "bf16", "bf16"), ("f32", "f32", "f32"),
                                       ("bf16", "f32", "bf16"), ("f32", "bf16", "bf16")])
-@pytest.mark.parametrize("M,D,pad", SHAPES)
+@pytest.mark.parametrize("M,D,pad", SHAPES + MANY)
 def test_norm_forward(M, D, pad, xt, wt, ht):
     x, w = rows(3, M, D, xt, pad), rows(4, 1, D, wt)[0].contiguous()
     G = O.groups(D)
@@ -134,7 +136,7 @@ def test_norm_forward(M, D, pad, xt, wt, ht):
 
 @pytest.mark.parametrize("dht,dxt,wt", [("f32", "bf16", "bf16"), ("f32", "f32", "f32"),
                                         ("bf16", "bf16", "f32"), ("bf16", "f32", "bf16")])
-@pytest.mark.parametrize("M,D,pad", SHAPES + [(601, 256, 0), (700, 40, 0), (400, 2048, 0)])
+@pytest.mark.parametrize("M,D,pad", SHAPES + MANY + [(601, 256, 0), (700, 40, 0), (400, 2048, 0)])
 def test_norm_backward(M, D, pad, dht, dxt, wt):
     x, w = rows(5, M, D, "f32"), rows(6, 1, D, wt)[0].contiguous()
     dh = rows(7, M, D, dht, pad, 1e-3)
