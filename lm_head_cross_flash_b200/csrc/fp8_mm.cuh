@@ -407,7 +407,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 
 // ------------------------------------------------------------- few rows --
 // NP: rows of a, padded (16, 32, 64, 128).  A stage holds 128 rows of b and
-// the NP rows of a for one group; four accumulators of NP columns.
+// the NP rows of a for one group; four accumulators of NP columns.  N = 128256,
+// K = 4096: 87.5 us with one row (6.0 TB/s, 91 % of the measured copy rate),
+// 114 us with 64; N = 73440, K = 1536 to fp32: 24 us with 16 rows, 29 us with
+// 61.  More stages (8 to 12 instead of 6 to 8) changed nothing.
 constexpr int FF_MAX_SCALES = 8192;  // NP * groups per CTA, kept in shared memory
 template <int NP>
 struct FfCfg {

@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x
 
 // ---------------------------------------------------------- quant blocks --
 // One CTA per 128x128 block: 256 threads hold 8 rows x 8 elements each (the
-// block is read once and stays in registers).
+// block is read once and stays in registers).  [73440, 1536] bf16: 64 us, 5.3
+// TB/s.
 template <bool VEC, typename T>
 __global__ void __launch_bounds__(256) quant_blocks_kernel(const T* __restrict__ x, int64_t ldx,
                                                            int64_t N, int K, QMat o) {
@@ -332,6 +333,10 @@ constexpr int norm_per_sm(int tpr, int r) {
 // threads hold a row in registers (R pieces of 8 elements each), so x is read
 // once; the codes of x and of h come from the same registers.  A block takes
 // row after row, the next one on its way while the current one is summed.
+// [8192, 2048] bf16 to H and checkpoint 19 us (4.4 TB/s), [32768, 4096] 135 us
+// (5.0 TB/s); bound by its instructions, 210 a warp and 256 elements (with
+// IEEE quotients in every thread and the weights read again for each row, 273
+// and 162 us).
 template <bool VEC, typename T, typename TH, int TPR, int R>
 __global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR, R))
     norm_fwd_kernel(const __grid_constant__ NormFwdArgs a) {
@@ -412,7 +417,9 @@ struct NormBwdArgs {
 // read once.  Every thread keeps the dw terms of its own columns in registers
 // over all of its rows; the blocks' parts are added in a fixed order by
 // norm_dw_kernel, so dw does not depend on timing.
-// The next row's loads are issued before the current row's sum.
+// The next row's loads are issued before the current row's sum.  [32768, 4096]
+// with fp32 dH 157 us (6.0 TB/s, 92 % of the measured copy rate); 244 us while
+// its registers let one block of 512 threads onto an SM instead of two.
 template <bool VEC, typename TX, typename TH, int TPR, int R>
 __global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR, R))
     norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {

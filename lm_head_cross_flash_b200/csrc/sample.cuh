@@ -30,6 +30,10 @@
 //    list takes is binned again, over its values or, where those are all
 //    equal, over its indices.  A step that does not halve it is followed by a
 //    bisection, so the search ends for every input.
+// Measured: one row of 73,440 fp32 logits 11 us; 256 rows of 262,144 bf16 45 us
+// greedy with logp (20 us of DRAM; 12 instructions a logit), 61 us with top-k
+// 50, 262 us with top-p 0.95 where most rows need more than the segments'
+// maxima say, 670 us where every row is flat.
 // Many rows run as two launches: the list with few CTAs a row (its fixed
 // costs, mostly waits, are paid by fewer CTAs), and the search with eight for
 // the rows that are left, so that one flat row does not hold up the batch.
