@@ -231,7 +231,6 @@ class Sampler {
   // search's warp cycles).
   template <typename W, typename F>
   __device__ void pass(int from, int to, W want, F f) const {
-    constexpr int NB = SA_SEG / 256;
     const int lane8 = int(threadIdx.x & 31) * 8;
     auto skip = [&](int i) {  // the first wanted segment from i on
       for (; i < to; i += SA_WARPS) {
@@ -551,6 +550,39 @@ class Sampler {
     return s < 1e30f ? s : 1e30f;
   }
 
+  // A ring of copies (cp.async), each thread's own, so that the loads of the
+  // next DEPTH segments are under way while one is worked on.  A segment is
+  // NB pieces of 256: eight logits a lane.
+  static constexpr int NB = SA_SEG / 256;
+  static constexpr int DEPTH = SA_RING / (SA_THREADS * 8 * int(sizeof(T)) * NB);
+  static_assert(DEPTH >= 2 && (DEPTH & (DEPTH - 1)) == 0, "a power of two");
+  __device__ uint4* slot(int p) const {
+    return reinterpret_cast<uint4*>(s_.ring) + threadIdx.x +
+           (p & (DEPTH - 1)) * (NB * int(sizeof(T) / 2) * SA_THREADS);
+  }
+  // The warp's p-th segment of the slice, on its way.
+  __device__ void copy_in(int p) const {
+    constexpr int PL = sizeof(T) / 2, STEP = SA_WARPS * SA_SEG;
+    const int c = s0_ + int(threadIdx.x >> 5) * SA_SEG + p * STEP, lane8 = int(threadIdx.x & 31) * 8;
+    if (c >= off_ && c + SA_SEG <= s1_) {
+      const uint32_t to = smem_u32(slot(p));
+      const uint4* from = reinterpret_cast<const uint4*>(g_ - off_ + c + lane8);
+#pragma unroll
+      for (int i = 0; i < NB * PL; ++i)
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
+                         to + i * SA_THREADS * 16),
+                     "l"(from + (i / PL) * 32 * PL + i % PL)
+                     : "memory");
+    } else if (c < s1_) {
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const SaRaw<T> r = fetch(c + k * 256 + lane8);
+#pragma unroll
+        for (int i = 0; i < PL; ++i) slot(p)[(k * PL + i) * SA_THREADS] = r.v[i];
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
   template <bool TAIL, bool Z>
   __device__ SaFirst first_pass(float cz);
   // 2^(c m - h): what a weight of 1 is in sums that are relative to h.
@@ -712,43 +744,15 @@ __device__ __forceinline__ float warp_max(float x) {
 template <typename T>
 template <bool TAIL, bool Z>
 __device__ SaFirst Sampler<T>::first_pass(float cz) {
-  constexpr int STEP = SA_WARPS * SA_SEG, NB = SA_SEG / 256;
+  constexpr int STEP = SA_WARPS * SA_SEG;
   constexpr float CT = 1.44269504f;  // log2(e)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float m = -INFINITY, ht = 0.f, hz = 0.f, least = INFINITY;
   int mi = 0x7FFFFFFF, ne = 0;
   double tail = 0.0, z = 0.0;
-  // A ring of copies (cp.async), each thread's own, so that the loads of the
-  // next DEPTH segments are under way while one is worked on.  A segment is
-  // NB pieces of 256: eight logits a lane.
-  constexpr int PL = sizeof(T) / 2, DEPTH = SA_RING / (SA_THREADS * 16 * PL * NB);
-  static_assert(DEPTH >= 2 && (DEPTH & (DEPTH - 1)) == 0, "a power of two");
+  constexpr int PL = sizeof(T) / 2;
   const int cw = s0_ + warp * SA_SEG;  // where the warp's first segment begins
   const int np = cw < s1_ ? (s1_ - cw + STEP - 1) / STEP : 0;
-  const int full = s1_ - cw >= SA_SEG ? (s1_ - cw - SA_SEG) / STEP + 1 : 0;
-  uint4* const ring = reinterpret_cast<uint4*>(s_.ring) + threadIdx.x;
-  auto slot = [&](int p) { return ring + (p & (DEPTH - 1)) * (NB * PL * SA_THREADS); };
-  auto issue = [&](int p) {
-    if (p < full && (p > 0 || cw >= off_)) {
-      const uint32_t to = smem_u32(slot(p));
-      const uint4* from = reinterpret_cast<const uint4*>(g_ - off_ + cw + p * STEP + lane * 8);
-#pragma unroll
-      for (int i = 0; i < NB * PL; ++i)
-        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(
-                         to + i * SA_THREADS * 16),
-                     "l"(from + (i / PL) * 32 * PL + i % PL)
-                     : "memory");
-    } else if (p < np) {
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const SaRaw<T> r = fetch(cw + p * STEP + k * 256 + lane * 8);
-#pragma unroll
-        for (int i = 0; i < PL; ++i) slot(p)[(k * PL + i) * SA_THREADS] = r.v[i];
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  for (int p = 0; p < DEPTH; ++p) issue(p);
   __syncthreads();  // what run() laid out in shared memory
   for (int p = 0; p < np; ++p) {
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
@@ -760,7 +764,7 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
       for (int i = 0; i < PL; ++i) r.v[i] = slot(p)[(k * PL + i) * SA_THREADS];
       raw_values<T>(r, v[k]);
     }
-    issue(p + DEPTH);
+    copy_in(p + DEPTH);
 #pragma unroll
     for (int k = 0; k < NB; ++k)
 #pragma unroll
@@ -927,7 +931,7 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
       s_.opened[atomicAdd(&s_.n_opened, 1)] = uint16_t(i);
   }
   __syncthreads();
-  constexpr int UN = 4, NB = SA_SEG / 256;
+  constexpr int UN = 4;
   const int n_opened = s_.n_opened;
   for (int i0 = threadIdx.x >> 5; i0 < n_opened * NB; i0 += SA_WARPS * UN) {
     SaRaw<T> r[UN];
@@ -1099,17 +1103,19 @@ __device__ void Sampler<T>::by_search(const Settings& o, const SaFirst& f) {
 template <typename T>
 template <int MODE>
 __device__ void Sampler<T>::run() {
-  if (threadIdx.x < 32) s_.pow2[threadIdx.x] = exp2(double(threadIdx.x) / 32.0);
+  for (int p = 0; p < DEPTH; ++p) copy_in(p);  // before anything is waited for
+  Settings o;
+  o.temp = a_.temperature == nullptr ? 1.f : a_.temperature[row_];
+  o.k = a_.top_k == nullptr ? 0 : a_.top_k[row_];
+  o.tp = a_.top_p == nullptr ? 1.f : a_.top_p[row_];
+  const float mp = a_.min_p == nullptr ? 0.f : a_.min_p[row_];
+  const float u = a_.u[row_];
   for (int i = threadIdx.x; i < SA_BINS; i += SA_THREADS) s_.open[i] = 0;
   for (int i = threadIdx.x; i < SA_MAX_SEGS; i += SA_THREADS) s_.segs[i] = 0;
   if (threadIdx.x == 0) s_.n_list = s_.n_opened = 0;
-  Settings o;
-  o.temp = a_.temperature == nullptr ? 1.f : a_.temperature[row_];
-  o.k = a_.top_k == nullptr ? 0 : max(a_.top_k[row_], 0);
-  if (o.k >= a_.V) o.k = 0;
-  o.tp = a_.top_p == nullptr ? 1.f : a_.top_p[row_];
-  const float mp = a_.min_p == nullptr ? 0.f : a_.min_p[row_];
-  o.u = double(fminf(fmaxf(a_.u[row_], 0.f), 1.f - 0x1p-24f));
+  if (threadIdx.x < 32) s_.pow2[threadIdx.x] = exp2(double(threadIdx.x) / 32.0);
+  o.k = o.k < 0 || o.k >= a_.V ? 0 : o.k;
+  o.u = double(fminf(fmaxf(u, 0.f), 1.f - 0x1p-24f));
   o.use_p = o.tp < 1.f;
   o.use_m = mp > 0.f;
   o.thr = o.use_m && mp < 1.f ? double(o.temp) * log(double(mp)) : 0.0;
