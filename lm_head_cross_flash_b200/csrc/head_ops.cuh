@@ -190,8 +190,6 @@ template <typename T>
 cce_status launch_sample_rows(const SampleArgs& a, int64_t B, cudaStream_t st) {
   const int c = sample_cluster(B, a.V, sm_count_guess());
   const int most = sample_cluster(1, a.V, sm_count_guess());
-  // Every rank fits the list: nothing is left to search.
-  if (a.V <= SA_CAP) return launch_sample<T, SA_LIST_ONLY>(a, B, 1, st);
   if (2 * c >= most) return launch_sample<T, SA_BOTH>(a, B, c, st);
   const cce_status s = launch_sample<T, SA_LIST_ONLY>(a, B, c, st);
   // Fewer CTAs a row where many rows may be left: 256 rows of 262,144 bf16

@@ -53,6 +53,7 @@ constexpr int SA_MAX_CLUSTER = 8;
 constexpr int SA_SEG = 512;        // logits that a warp reads at once: one segment
 constexpr int SA_MAX_SEGS = 1024;  // segments (or groups of them) of one CTA
 constexpr int SA_OPEN = 128;       // segments that the list opens if their mass is not enough
+constexpr int SA_COUNT_SLICE = 16384; // logits of a CTA up to which the list counts them all
 constexpr int SA_RING = 64 * 1024; // copies in flight during the first pass
 constexpr int SA_FLUSH = 65536;    // logits that 15-bit digits can be summed over in 32 bits
 constexpr int SA_UNDECIDED = -2;   // token of a row that the first launch leaves to the second,
@@ -162,6 +163,17 @@ __device__ __forceinline__ void raw_values(const SaRaw<T>& r, float (&v)[8]) {
   }
 }
 
+// 2^(j/32), rounded to nearest.
+__device__ const double SA_POW2[32] = {
+    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
+    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
+    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
+    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
+    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
+    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0};
+
 template <typename T>
 class Sampler {
  public:
@@ -263,16 +275,21 @@ class Sampler {
   __device__ void pass(F f) const {
     pass(0, n_segs(), [](uint32_t) { return true; }, f);
   }
-  // The logits of a piece that hit() takes, one by one (few of many).
-  template <typename H, typename F>
-  __device__ void each_hit(const float (&v)[8], int c, H hit, F f) const {
+  // The logits of a lane's piece that hit() takes, as bits (c: the first one's
+  // index).
+  template <typename H>
+  __device__ uint32_t hits(const float (&v)[8], int c, H hit) const {
     uint32_t mask = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) mask |= uint32_t(v[j] > -INFINITY && hit(v[j], c + j)) << j;
-    for (; mask != 0; mask &= mask - 1) {
-      const int j = __ffs(mask) - 1;
-      f(rank_of(to_f32(g_[c + j]), c + j));
-    }
+    return mask;
+  }
+  // Calls f with the rank of each of them.
+  template <typename F>
+  __device__ static void each(uint32_t mask, const float (&v)[8], int c, F f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (mask >> j & 1) f(rank_of(v[j], c + j));
   }
 
   __device__ float below(float l) const { return l == max_ ? 0.f : max_ - l; }
@@ -351,7 +368,7 @@ class Sampler {
     auto clear = [&](bool counts) {
       for (int i = threadIdx.x; i < SA_BINS; i += SA_THREADS) {
         if (counts) s_.hist[i] = 0;
-        s_.dig[0][i] = s_.dig[1][i] = s_.dig[2][i] = 0;
+        if (by_mass) s_.dig[0][i] = s_.dig[1][i] = s_.dig[2][i] = 0;
       }
     };
     auto digits = [&](int r, int b) -> u64 {
@@ -379,6 +396,7 @@ class Sampler {
           atomicAdd(&s_.dig[2][b], uint32_t(w >> 30));
         }
       });
+      if (!by_mass) continue;
       cl_.sync();
       for (int k = 0, i = threadIdx.x; i < n; ++k, i += SA_THREADS) {
         u64 x = 0;
@@ -392,6 +410,7 @@ class Sampler {
         clear(false);
       }
     }
+    if (!by_mass) cl_.sync();
     for (int k = 0, i = threadIdx.x; i < n; ++k, i += SA_THREADS) {
       uint32_t x = 0;
       u64 y = 0;
@@ -436,65 +455,111 @@ class Sampler {
     __syncthreads();
   }
 
-  // Candidates go to the first CTA's list.
-  __device__ void append(u64 r) {
-    const int i = atomicAdd(cl_.map_shared_rank(&s_.n_list, 0), 1);
-    if (i < SA_CAP) cl_.map_shared_rank(s_.list, 0)[i] = r;
+  // A warp's candidates go to the first CTA's list, with one addition to its
+  // length (one for each candidate took 10 us of 25 at 2,048 candidates).
+  __device__ void append(uint32_t mask, const float (&v)[8], int c) {
+    if (__ballot_sync(0xffffffffu, mask != 0) == 0) return;
+    const int lane = threadIdx.x & 31, n = __popc(mask);
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    int at = 0;
+    if (lane == 31) at = atomicAdd(cl_.map_shared_rank(&s_.n_list, 0), upto);
+    at = __shfl_sync(0xffffffffu, at, 31) + upto - n;
+    u64* list = cl_.map_shared_rank(s_.list, 0);
+    each(mask, v, c, [&](u64 r) {
+      if (at < SA_CAP) list[at] = r;
+      ++at;
+    });
   }
   // First CTA: sorts the list from the highest rank down; its length.  Thread
-  // t gets the ranks 4t to 4t + 3.  A bitonic network: strides below 4 stay in
-  // a thread, those below 128 in a warp (shuffles), the others go through the
-  // list's memory.
+  // t gets the ranks 4t to 4t + 3.
   __device__ int sort_list(u64 (&r)[4]) {
     const int n = min(s_.n_list, SA_CAP), e0 = threadIdx.x * 4;
+    if (n <= SA_THREADS) {
+      // Few: an element's place is the number of those above it.  The threads
+      // are spread over elements and parts of the list (2,000 cycles at 256,
+      // where the network below took 7,000).
+      int np = 32;
+      while (np < n) np *= 2;
+      const int parts = SA_THREADS / np, e = threadIdx.x & (np - 1), part = threadIdx.x / np;
+      for (int i = threadIdx.x; i < np; i += SA_THREADS) {
+        s_.open[i] = 0;
+        if (i >= n) s_.list[i] = 0;
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) s_.n_list = 0;  // for the next list
+      const u64 x = s_.list[e];
+      const int len = (n + parts - 1) / parts, to = min(n, (part + 1) * len);
+      int above = 0;
+#pragma unroll 4
+      for (int j = part * len; j < to; ++j) above += s_.list[j] > x;
+      if (e < n) atomicAdd(&s_.open[e], uint32_t(above));
+      __syncthreads();
+      if (part == 0 && e < n) s_.list[SA_CAP / 2 + s_.open[e]] = x;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        r[i] = e0 + i < n ? s_.list[SA_CAP / 2 + e0 + i] : 0;
+        if (e0 + i < n) s_.list[e0 + i] = r[i];
+      }
+      __syncthreads();
+      return n;
+    }
+    // A bitonic network: strides below 4 stay in a thread, those below 128 in a
+    // warp (shuffles), the others go through the list's memory.
     int len = 128;
     while (len < n) len *= 2;
     const bool in = e0 < len;  // the same for a whole warp
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = e0 + i < n ? s_.list[e0 + i] : 0;
     __syncthreads();
-    if (threadIdx.x == 0) s_.n_list = 0;  // for the next list
+    if (threadIdx.x == 0) s_.n_list = 0;
     auto order = [](u64& x, u64& y, bool down) {
       const u64 a = x, b = y;
-      if ((a < b) == down) {
-        x = b;
-        y = a;
-      }
+      const bool swap = (a < b) == down;
+      x = swap ? b : a;
+      y = swap ? a : b;
     };
-    for (int k = 2; k <= len; k *= 2)
-      for (int j = k / 2; j > 0; j /= 2) {
-        if (j >= 128) {
-          if (in) {
+    for (int k = 2; k <= len; k *= 2) {
+      const bool down = (e0 & k) == 0;
+      for (int j = k / 2; j >= 128; j /= 2) {
+        if (in) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s_.list[e0 + i] = r[i];
-          }
-          __syncthreads();
-          if (in) {
-            const bool most = ((e0 & k) == 0) == ((e0 & j) == 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const u64 o = s_.list[(e0 ^ j) + i];
-              r[i] = most ? max(r[i], o) : min(r[i], o);
-            }
-          }
-          __syncthreads();
-        } else if (!in) {
-          continue;
-        } else if (j >= 4) {
-          const bool most = ((e0 & k) == 0) == ((e0 & j) == 0);
+          for (int i = 0; i < 4; ++i) s_.list[e0 + i] = r[i];
+        }
+        __syncthreads();
+        if (in) {
+          const bool most = down == ((e0 & j) == 0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const u64 o = __shfl_xor_sync(0xffffffffu, r[i], j / 4);
-            r[i] = most ? max(r[i], o) : min(r[i], o);
+            const u64 o = s_.list[(e0 ^ j) + i];
+            r[i] = (o > r[i]) == most ? o : r[i];
           }
-        } else if (j == 2) {
-          order(r[0], r[2], (e0 & k) == 0);
-          order(r[1], r[3], (e0 & k) == 0);
-        } else {
-          order(r[0], r[1], (e0 & k) == 0);
-          order(r[2], r[3], ((e0 + 2) & k) == 0);
+        }
+        __syncthreads();
+      }
+      if (!in) continue;
+#pragma unroll
+      for (int j = 64; j >= 4; j /= 2) {
+        if (j >= k) continue;
+        const bool most = down == ((e0 & j) == 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const u64 o = __shfl_xor_sync(0xffffffffu, r[i], j / 4);
+          r[i] = (o > r[i]) == most ? o : r[i];
         }
       }
+      if (k > 2) {
+        order(r[0], r[2], down);
+        order(r[1], r[3], down);
+      }
+      order(r[0], r[1], down);
+      order(r[2], r[3], ((e0 + 2) & k) == 0);
+    }
     if (in) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) s_.list[e0 + i] = r[i];
@@ -585,10 +650,13 @@ class Sampler {
   }
   template <bool TAIL, bool Z>
   __device__ SaFirst first_pass(float cz);
-  // 2^(c m - h): what a weight of 1 is in sums that are relative to h.
-  __device__ static double unround(float m, float c, float h) {
+  // 2^(c m - h): what a weight of 1 is in sums that are relative to h, or with
+  // sign -1 its inverse.  The difference is a rounding error, so two terms of
+  // the series are enough.
+  __device__ static double unround(float m, float c, float h, double sign = 1.0) {
     const float d = fmaf(m, c, -h);
-    return fabsf(d) < 1.f ? 1.0 + double(d) * 0.6931471805599453 : 1.0;
+    const double x = fabsf(d) < 1.f ? sign * double(d) * 0.6931471805599453 : 0.0;
+    return 1.0 + x * (1.0 + 0.5 * x);
   }
   struct Settings {
     float temp, tp;
@@ -674,14 +742,14 @@ __device__ void Sampler<T>::search(bool by_mass, u64 target) {
           return step == 0 ? bin_of(key_value(key)) <= here : key >= uint32_t(bottom0 >> 32);
         },
         [&](const float (&v)[8], int c) {
-          each_hit(v, c, [&](float l, int i) { return bin(l, i) == here; }, [&](u64 r) {
-            if (fits) {
-              append(r);
-            } else {
+          const uint32_t mask = hits(v, c, [&](float l, int i) { return bin(l, i) == here; });
+          if (fits)
+            append(mask, v, c);
+          else
+            each(mask, v, c, [&](u64 r) {
               p.hi = max(p.hi, r);
               p.lo = min(p.lo, r);
-            }
-          });
+            });
         });
     if (fits) break;
     p = exchange(p);
@@ -824,8 +892,8 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
     if (TAIL) tail += double(sum_t);
     if (Z) z += double(sum_z);
   }
-  tail /= unround(m, CT, ht);
-  z /= unround(m, cz, hz);
+  if (TAIL) tail *= unround(m, CT, ht, -1.0);
+  if (Z) z *= unround(m, cz, hz, -1.0);
   // threads -> CTA
   SaFirst f;
   f.hi = mi != 0x7FFFFFFF ? rank_of(m, mi) : 0;
@@ -881,47 +949,75 @@ template <typename T>
 __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
   // Bins between the maximum and the least of the segments' maxima, which
   // falls short of the last bin; that one takes what is below.
-  const float scale = scale_for(below(f.least)) * 0.996f;
+  float scale = scale_for(below(f.least)) * 0.996f;
   int last;  // candidates: the logits in bins up to this one
-  const bool all = a_.V <= SA_CAP;
-  if (all) {
-    last = SA_BINS;
-  } else if (o.use_m && !o.use_p && o.k == 0) {
+  bool all = false;
+  if (o.use_m && !o.use_p && o.k == 0) {
     last = int(fmin(floor(-o.thr * (1.0 + 0x1p-20) * double(scale)) + 1.0, double(SA_BINS)));
   } else {
-    // top-k: the bin of the k-th largest maximum, which k logits reach.
-    // Otherwise: the bin down to which the maxima alone have the mass that is
-    // asked for, or that of the SA_OPEN-th largest, or of the least.
-    if (o.k > SA_CAP / 2) return false;
+    // top-k: the bin of the k-th rank; else the bin down to which there is the
+    // mass that is asked for.  From the maxima alone if those are enough (of
+    // each segment that reaches a bin one logit is known to be there).  If not,
+    // from the counts of all logits where a CTA has few of them (4,096 logits,
+    // top-k 50: 30 us without), else the SA_OPEN largest segments are opened.
+    const double part = (o.use_p ? double(fmaxf(o.tp, 0.f)) : o.u) * (1.0 + SA_SUM_ERROR);
+    const u64 mass = u64(part * (double(f.n) + f.z) * 0x1p20) + 2;
+    // The bin in which the count or the mass reaches `want`, or -1; n_in: the
+    // count up to it.
+    auto reach = [&](uint4 n4, bool count, u64 want) {
+      const uint32_t n[4] = {n4.x, n4.y, n4.z, n4.w};
+      u64 m[4], sum = 0, cnt = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // a weight at the bin's far end, rounded down; the last bin has no end
+        const int b = threadIdx.x * 4 + i;
+        const float x = float(b + 1) / scale * float(-c_);
+        const u64 w = b < SA_BINS - 1 ? u64(ex2_approx(x) * 0x1p20f * 0.99f) : 0;
+        cnt += n[i];
+        m[i] = sum += count ? u64(n[i]) : n[i] * w;
+      }
+      if (threadIdx.x == 0) s_.bin = -1;
+      __syncthreads();
+      const u64 before = scan(sum, s_.warp_sum[0]) - sum;
+      u64 upto = scan(cnt, s_.warp_sum[1]) - cnt;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        upto += n[i];
+        if (before + m[i] >= want && before + (i ? m[i - 1] : 0) < want) {
+          s_.bin = threadIdx.x * 4 + i;
+          s_.n_in = uint32_t(upto);
+        }
+      }
+      __syncthreads();
+      const int b = s_.bin;
+      __syncthreads();
+      return b;
+    };
+    if (o.k > SA_CAP / 2 && a_.V > SA_CAP) return false;
     const int n_maxima = (n_segs() + a_.seg_mul - 1) / a_.seg_mul;
     uint32_t* open = cl_.map_shared_rank(s_.open, 0);
     for (int i = threadIdx.x; i < n_maxima; i += SA_THREADS)
       if (s_.segs[i] != 0) atomicAdd(&open[bin_below(max_, key_value(s_.segs[i]), scale)], 1u);
     cl_.sync();
-    const uint4 n4 = reinterpret_cast<const uint4*>(open)[threadIdx.x];
-    const uint32_t n1[4] = {n4.x, n4.y, n4.z, n4.w};
-    const double part = (o.use_p ? double(fmaxf(o.tp, 0.f)) : o.u) * (1.0 + SA_SUM_ERROR);
-    const u64 mass = u64(part * (double(f.n) + f.z) * 0x1p20) + 2;
-    const u64 want = o.k > 0 ? o.k : SA_OPEN;
-    u64 n[4], w[4], sn = 0, sw = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      n[i] = sn += n1[i];
-      // a weight at the bin's far end, rounded down
-      const float x = float(threadIdx.x * 4 + i + 1) / scale * float(-c_);
-      w[i] = sw += n1[i] ? u64(n1[i] * (ex2_approx(x) * 0x1p20f * 0.99f)) : 0;
+    const uint4 maxima = reinterpret_cast<const uint4*>(open)[threadIdx.x];
+    last = reach(maxima, o.k > 0, o.k > 0 ? u64(o.k) : mass);
+    if (last < 0 && a_.slice <= SA_COUNT_SLICE) {
+      // twice as far down as the least of the maxima
+      scale *= 0.5f;
+      bin_up(false, [](uint32_t) { return true; },
+             [&](float l, int) { return bin_below(max_, l, scale); });
+      last = reach(reinterpret_cast<const uint4*>(s_.tot)[threadIdx.x], o.k > 0,
+                   o.k > 0 ? u64(o.k) : mass);
+      if (last < 0 && a_.V <= SA_CAP) {
+        last = SA_BINS;
+        all = true;
+      } else if (last < 0 || s_.n_in > SA_CAP) {
+        return false;
+      }
+    } else if (last < 0) {
+      last = o.k > 0 ? -1 : reach(maxima, true, SA_OPEN);
+      if (last < 0) last = bin_below(max_, f.least, scale);
     }
-    if (threadIdx.x == 0) s_.bin = s_.done = bin_below(max_, f.least, scale);
-    __syncthreads();
-    const u64 bn = scan(sn, s_.warp_sum[0]) - sn, bw = scan(sw, s_.warp_sum[1]) - sw;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = threadIdx.x * 4 + i;
-      if (bn + n[i] >= want && bn + (i ? n[i - 1] : 0) < want) s_.bin = b;
-      if (o.k == 0 && bw + w[i] >= mass && bw + (i ? w[i - 1] : 0) < mass) s_.done = b;
-    }
-    __syncthreads();
-    last = o.k == 0 ? (s_.done < bin_below(max_, f.least, scale) ? s_.done : s_.bin) : s_.bin;
     __syncthreads();
   }
   // the segments that reach that far, then their logits
@@ -947,11 +1043,13 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
     }
 #pragma unroll
     for (int k = 0; k < UN; ++k) {
-      if (c[k] >= s1_) continue;
-      float v[8];
-      raw_values<T>(r[k], v);
-      each_hit(v, c[k] - off_, [&](float l, int) { return bin_below(max_, l, scale) <= last; },
-               [&](u64 q) { append(q); });
+      float v[8] = {};
+      uint32_t mask = 0;
+      if (c[k] < s1_) {
+        raw_values<T>(r[k], v);
+        mask = hits(v, c[k] - off_, [&](float l, int) { return bin_below(max_, l, scale) <= last; });
+      }
+      append(mask, v, c[k] - off_);
     }
   }
   const double unit = double(u64(1) << a_.bits);
@@ -1042,8 +1140,7 @@ __device__ void Sampler<T>::by_search(const Settings& o, const SaFirst& f) {
     pass(
         0, n_segs(), [&](uint32_t key) { return bin_below(max_, key_value(key), scale) <= last; },
         [&](const float (&v)[8], int c) {
-          each_hit(v, c, [&](float l, int) { return bin_below(max_, l, scale) <= last; },
-                   [&](u64 r) { append(r); });
+          append(hits(v, c, [&](float l, int) { return bin_below(max_, l, scale) <= last; }), v, c);
         });
     return finish(p, Total{true, keep, 0.0, 0.0}, false);
   };
@@ -1113,7 +1210,7 @@ __device__ void Sampler<T>::run() {
   for (int i = threadIdx.x; i < SA_BINS; i += SA_THREADS) s_.open[i] = 0;
   for (int i = threadIdx.x; i < SA_MAX_SEGS; i += SA_THREADS) s_.segs[i] = 0;
   if (threadIdx.x == 0) s_.n_list = s_.n_opened = 0;
-  if (threadIdx.x < 32) s_.pow2[threadIdx.x] = exp2(double(threadIdx.x) / 32.0);
+  if (threadIdx.x < 32) s_.pow2[threadIdx.x] = SA_POW2[threadIdx.x];
   o.k = o.k < 0 || o.k >= a_.V ? 0 : o.k;
   o.u = double(fminf(fmaxf(u, 0.f), 1.f - 0x1p-24f));
   o.use_p = o.tp < 1.f;
