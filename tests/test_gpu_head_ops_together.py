@@ -200,3 +200,56 @@ def test_two_streams_at_once():
     for b in bufs[1:]:
         assert torch.equal(b.tokens, bufs[0].tokens) and torch.equal(b.logp, bufs[0].logp)
         assert torch.equal(b.logits, bufs[0].logits)
+
+
+def far(x):
+    """The same values with rows 2^30 elements apart: offsets pass 32 bits."""
+    rows, cols = x.shape
+    y = torch.empty((rows - 1) * 2 ** 30 + cols, dtype=x.dtype, device="cuda")
+    y = y.as_strided((rows, cols), (2 ** 30, 1))
+    y.copy_(x)
+    return y
+
+
+def test_rows_far_apart():
+    """Every matrix with a row stride of 2^30 gives what dense rows give."""
+    M, D, V = 4, 256, 3000
+    X, w, W, u = make(6, M, D, V)
+    G = cce.fp8_groups(D)
+    f32 = lambda *s: torch.empty(*s, device="cuda")
+    codes = lambda r, c: cce.fp8_empty(r, c).zero_()
+
+    def run(wrap):
+        x, h = wrap(X), wrap(torch.zeros_like(X))
+        x8, xs, rstd, h8, hs = wrap(codes(M, D)), f32(M, G), f32(M), wrap(codes(M, D)), f32(M, G)
+        cce.cce_norm_forward(x, w, EPS, h, h8, hs, x8, xs, rstd)
+        dh, dx, dw = wrap(X.float()), wrap(torch.zeros_like(X)), f32(D)
+        ws = torch.zeros(cce.cce_norm_backward_workspace_bytes(M, D), dtype=torch.uint8, device="cuda")
+        cce.cce_norm_backward(x8, xs, rstd, w, dh, dx, dw, ws)
+        q, s = wrap(codes(M, D)), f32(M, G)
+        cce.cce_fp8_quant_rows(x, q, s)
+        wq, wsc = wrap(codes(M, D)), f32(1, G)
+        cce.cce_fp8_quant_blocks(x, wq, wsc)
+        few, st = wrap(torch.zeros(M, M, device="cuda")), torch.zeros(256, dtype=torch.uint8, device="cuda")
+        cce.cce_fp8_matmul(h8, hs, wq, wsc, few, st)
+        head = cce.Fp8Head.from_dense(W)
+        logits = wrap(torch.zeros(M, V, device="cuda"))
+        cce.cce_fp8_matmul(h8, hs, head.q, head.s, logits, st)
+        tok, lp = torch.zeros(M, dtype=torch.int32, device="cuda"), f32(M)
+        cce.cce_sample_rows(logits, None, None, torch.full((M,), 0.9, device="cuda"), None, u[:M], tok, lp)
+        torch.cuda.synchronize()
+        return [t.float().cpu() for t in (h, x8, xs, rstd, h8, hs, dx, dw, q, s, wq, wsc, few, logits, tok, lp)]
+
+    for a, b in zip(run(lambda t: t), run(far)):
+        assert torch.equal(a, b)
+    # the many-rows product: C's rows far apart (130 rows would need 520 GB at
+    # that stride, so theirs is 2^25: the last row begins beyond 2^32)
+    A, B = make(7, 130, D, 200)[0], make(8, 10, D, 200)[2]
+    a8, sa = codes(130, D), f32(130, G)
+    cce.cce_fp8_quant_rows(A, a8, sa)
+    hb = cce.Fp8Head.from_dense(B)
+    st = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    dense, wide = f32(130, 200), torch.empty(129 * 2 ** 25 + 200, device="cuda").as_strided((130, 200), (2 ** 25, 1))
+    cce.cce_fp8_matmul(a8, sa, hb.q, hb.s, dense, st)
+    cce.cce_fp8_matmul(a8, sa, hb.q, hb.s, wide, st)
+    assert torch.equal(dense, wide)
