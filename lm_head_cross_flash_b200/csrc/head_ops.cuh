@@ -184,8 +184,8 @@ cce_status launch_sample(SampleArgs a, int64_t B, int c, cudaStream_t st) {
 }
 
 // One launch where a row gets nearly as many CTAs as it can use, else two (256
-// rows of 262,144 bf16 logits with top-k 50: 67 us with one CTA a row, 165 us
-// with eight).
+// rows of 262,144 bf16 logits with top-k 50: 62 us with one CTA a row, 82 with
+// two, 165 with eight).
 template <typename T>
 cce_status launch_sample_rows(const SampleArgs& a, int64_t B, cudaStream_t st) {
   const int c = sample_cluster(B, a.V, sm_count_guess());
@@ -193,8 +193,8 @@ cce_status launch_sample_rows(const SampleArgs& a, int64_t B, cudaStream_t st) {
   if (2 * c >= most) return launch_sample<T, SA_BOTH>(a, B, c, st);
   const cce_status s = launch_sample<T, SA_LIST_ONLY>(a, B, c, st);
   // Fewer CTAs a row where many rows may be left: 256 rows of 262,144 bf16
-  // logits, all of them flat, take 627 us with 2, 782 with 4, 1134 with 8; but
-  // 61 rows of 128,256, few of them flat, 74 us with 8 and 102 with 2.
+  // logits, all of them flat, take 657 us with 2 and 827 with 4; but 61 rows of
+  // 128,256, few of them flat, 74 us with 8 and 102 with 2.
   int cs = most;
   while (cs > 1 && cs * B > 4 * sm_count_guess()) cs /= 2;
   return s != CCE_OK ? s : launch_sample<T, SA_SEARCH_ONLY>(a, B, cs, st);

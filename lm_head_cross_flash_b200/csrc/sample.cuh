@@ -30,10 +30,10 @@
 //    list takes is binned again, over its values or, where those are all
 //    equal, over its indices.  A step that does not halve it is followed by a
 //    bisection, so the search ends for every input.
-// Measured: one row of 73,440 fp32 logits 11 us; 256 rows of 262,144 bf16 45 us
-// greedy with logp (20 us of DRAM; 12 instructions a logit), 61 us with top-k
-// 50, 262 us with top-p 0.95 where most rows need more than the segments'
-// maxima say, 670 us where every row is flat.
+// Measured: one row of 73,440 fp32 logits 10.4 us; 256 rows of 262,144 bf16 45
+// us greedy with logp (20 us of DRAM; 12 instructions a logit), 62 us with
+// top-k 50, 277 us with top-p 0.95 where a fifth of the rows is flat, 657 us
+// where all are.
 // Many rows run as two launches: the list with few CTAs a row (its fixed
 // costs, mostly waits, are paid by fewer CTAs), and the search with eight for
 // the rows that are left, so that one flat row does not hold up the batch.
@@ -456,7 +456,8 @@ class Sampler {
   }
 
   // A warp's candidates go to the first CTA's list, with one addition to its
-  // length (one for each candidate took 10 us of 25 at 2,048 candidates).
+  // length (with one for each candidate, 215 flat rows of 145,242 bf16 logits,
+  // whose bins hold many equal ones, took 636 us instead of 346).
   __device__ void append(uint32_t mask, const float (&v)[8], int c) {
     if (__ballot_sync(0xffffffffu, mask != 0) == 0) return;
     const int lane = threadIdx.x & 31, n = __popc(mask);
@@ -481,8 +482,8 @@ class Sampler {
     const int n = min(s_.n_list, SA_CAP), e0 = threadIdx.x * 4;
     if (n <= SA_THREADS) {
       // Few: an element's place is the number of those above it.  The threads
-      // are spread over elements and parts of the list (2,000 cycles at 256,
-      // where the network below took 7,000).
+      // are spread over elements and parts of the list (a network over 128 took
+      // 7,000 cycles, over 2,048 29,000).
       int np = 32;
       while (np < n) np *= 2;
       const int parts = SA_THREADS / np, e = threadIdx.x & (np - 1), part = threadIdx.x / np;
