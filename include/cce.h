@@ -615,7 +615,8 @@ cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs,
  * cce_forward's logp for that label (0 for token -1).
  * Masses are sums of fixed-point numbers (weights in fp64, rounded to
  * 2^-45, for V above 2^18 to 2^-(63 - ceil(log2 V))), so the tokens do not
- * depend on the order of summation.  One kernel, no workspace.
+ * depend on the order of summation.  One or two kernels, no workspace; until
+ * the last is done, tokens may hold other negative numbers.
  */
 cce_status cce_sample_rows(const void* logits, cce_dtype dtype, int64_t B,
                            int64_t V, int64_t ld, const float* temperature,

@@ -183,14 +183,17 @@ cce_status launch_sample(SampleArgs a, int64_t B, int c, cudaStream_t st) {
              : (cudaGetLastError(), CCE_ERR_CUDA);
 }
 
-// One launch where a row gets nearly as many CTAs as it can use, else two (256
+// One launch where a row gets nearly as many CTAs as it can use and there are
+// few rounds of them (the list alone runs two CTAs on an SM: 4,000 rows of
+// 1,000 logits 370 us, 500 in one launch), else two (256
 // rows of 262,144 bf16 logits with top-k 50: 62 us with one CTA a row, 82 with
 // two, 165 with eight).
 template <typename T>
 cce_status launch_sample_rows(const SampleArgs& a, int64_t B, cudaStream_t st) {
   const int c = sample_cluster(B, a.V, sm_count_guess());
   const int most = sample_cluster(1, a.V, sm_count_guess());
-  if (2 * c >= most) return launch_sample<T, SA_BOTH>(a, B, c, st);
+  if (2 * c >= most && c * B <= 2 * sm_count_guess())
+    return launch_sample<T, SA_BOTH>(a, B, c, st);
   const cce_status s = launch_sample<T, SA_LIST_ONLY>(a, B, c, st);
   // Fewer CTAs a row where many rows may be left: 256 rows of 262,144 bf16
   // logits, all of them flat, take 657 us with 2 and 827 with 4; but 61 rows of

@@ -97,6 +97,15 @@ def test_large_vocabularies(B, V, spread, peaks, dtype):
     check(l, k=[V // 2] * B, p=[0.9] * B, u=n)
 
 
+@pytest.mark.parametrize("B,V,spread,dtype", [(1500, 300, 2.5, BF), (400, 5000, 4.0, F),
+                                              (350, 20000, 1.0, F), (200, 40001, 1.0, BF)])
+def test_more_rows_than_run_at_once(B, V, spread, dtype):
+    """Flat rows among others: the search's clusters take several rows each."""
+    l = logits(V, B, V, dtype, spread, False)
+    check(l, **settings(V, B))
+    check(l, p=[0.9] * B, u=np.random.default_rng(2).random(B).astype(np.float32))
+
+
 def test_rows_without_and_with_one_live_logit():
     l = torch.full((6, 5000), float("-inf"), device="cuda")
     l[1, 4999] = -1e30
