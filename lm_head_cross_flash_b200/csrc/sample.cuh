@@ -322,6 +322,11 @@ class Sampler {
   }
 
   // ------------------------------------------------- block and cluster --
+  // A barrier of the cluster (of the block where that is all of it).
+  __device__ void meet() {
+    if (C_ == 1) __syncthreads();
+    else cl_.sync();
+  }
   __device__ static SaPart nothing() { return SaPart{0, ~u64(0), 0}; }
   __device__ static SaPart merge_lanes(SaPart p, int o) {
     p.hi = max(p.hi, __shfl_xor_sync(0xffffffffu, p.hi, o));
@@ -341,7 +346,7 @@ class Sampler {
       for (int o = SA_WARPS / 2; o > 0; o >>= 1) p = merge_lanes(p, o);
       if (lane < C_) *cl_.map_shared_rank(&s_.parts[turn_][me_], lane) = p;
     }
-    cl_.sync();
+    meet();
     p = s_.parts[turn_][lane & (C_ - 1)];
     for (int o = C_ / 2; o > 0; o >>= 1) p = merge_lanes(p, o);
     turn_ ^= 1;
@@ -397,7 +402,7 @@ class Sampler {
         }
       });
       if (!by_mass) continue;
-      cl_.sync();
+      meet();
       for (int k = 0, i = threadIdx.x; i < n; ++k, i += SA_THREADS) {
         u64 x = 0;
         for (int r = 0; r < C_; ++r) x += digits(r, b0 + i);
@@ -406,11 +411,11 @@ class Sampler {
           if (q == k) sum[q] += x;
       }
       if (from + SA_FLUSH / SA_SEG < end) {
-        cl_.sync();
+        meet();
         clear(false);
       }
     }
-    if (!by_mass) cl_.sync();
+    if (!by_mass) meet();
     for (int k = 0, i = threadIdx.x; i < n; ++k, i += SA_THREADS) {
       uint32_t x = 0;
       u64 y = 0;
@@ -423,7 +428,7 @@ class Sampler {
         *cl_.map_shared_rank(&s_.mass[b0 + i], r) = y;
       }
     }
-    cl_.sync();
+    meet();
   }
 
   __device__ void bin_level0() {
@@ -604,7 +609,7 @@ class Sampler {
       *cl_.map_shared_rank(&s_.res_rank, threadIdx.x) = s_.res_rank;
       *cl_.map_shared_rank(&s_.res_cum, threadIdx.x) = s_.res_cum;
     }
-    cl_.sync();
+    meet();
   }
 
   // Bins of equal width below the value vt, the last one open.
@@ -784,7 +789,7 @@ __device__ void Sampler<T>::search(bool by_mass, u64 target) {
     }
     level0_ = false;
   }
-  cl_.sync();
+  meet();
   if (me_ == 0) {
     u64 r[4];
     const int n = sort_list(r);
@@ -942,7 +947,7 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
     f = join(s_.warp_first[lane & (SA_WARPS - 1)], SA_WARPS);
     if (lane < C_) *cl_.map_shared_rank(&s_.firsts[me_], lane) = f;
   }
-  cl_.sync();
+  meet();
   return join(s_.firsts[lane & (C_ - 1)], C_);
 }
 
@@ -999,7 +1004,7 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
     uint32_t* open = cl_.map_shared_rank(s_.open, 0);
     for (int i = threadIdx.x; i < n_maxima; i += SA_THREADS)
       if (s_.segs[i] != 0) atomicAdd(&open[bin_below(max_, key_value(s_.segs[i]), scale)], 1u);
-    cl_.sync();
+    meet();
     const uint4 maxima = reinterpret_cast<const uint4*>(open)[threadIdx.x];
     last = reach(maxima, o.k > 0, o.k > 0 ? u64(o.k) : mass);
     if (last < 0 && a_.slice <= SA_COUNT_SLICE) {
@@ -1064,7 +1069,7 @@ __device__ bool Sampler<T>::by_list(const Settings& o, const SaFirst& f) {
 
 template <typename T>
 __device__ bool Sampler<T>::finish(const Settings& o, const Total& z, bool all) {
-  cl_.sync();
+  meet();
   if (me_ == 0) {
     bool ok = s_.n_list <= SA_CAP;
     if (ok) {
@@ -1120,7 +1125,7 @@ __device__ bool Sampler<T>::finish(const Settings& o, const Total& z, bool all) 
     if (threadIdx.x == 0) s_.n_list = 0;  // it may have run over
     if (int(threadIdx.x) < C_) *cl_.map_shared_rank(&s_.done, threadIdx.x) = ok;
   }
-  cl_.sync();
+  meet();
   return s_.done;
 }
 
@@ -1153,7 +1158,7 @@ __device__ void Sampler<T>::by_search(const Settings& o, const SaFirst& f) {
     locate(false, u64(o.k));
     const int last = s_.bin;
     if (s_.base + s_.n_in >= u64(o.k) && settled(o, last, scale, 0)) return;
-    cl_.sync();  // the counts have been read
+    meet();  // the counts have been read
   }
   // Bins over 24 T: what lies below has less than 4e-11 of the largest weight
   // each, and falls into the last bin.
