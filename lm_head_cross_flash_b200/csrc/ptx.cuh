@@ -344,6 +344,14 @@ __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release;\n\t"
                "barrier.cluster.wait.acquire;" ::: "memory");
 }
+// The same barrier in two halves, for CTAs that only have to know that all of
+// the cluster runs before they touch one another's shared memory.
+__device__ __forceinline__ void cluster_arrive_started() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 
 // TMA load of one CTA of a pair whose completion is counted on the leader
 // CTA's mbarrier (`bar_cluster`: shared::cluster address).

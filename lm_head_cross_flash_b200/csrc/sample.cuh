@@ -177,8 +177,10 @@ __device__ const double SA_POW2[32] = {
 template <typename T>
 class Sampler {
  public:
-  __device__ Sampler(const SampleArgs& a, SaShared& s, int row)
-      : a_(a), s_(s), cl_(cooperative_groups::this_cluster()) {
+  // all_run: every CTA of the cluster is known to run already; otherwise the
+  // kernel has arrived on the cluster's barrier and the first pass waits.
+  __device__ Sampler(const SampleArgs& a, SaShared& s, int row, bool all_run)
+      : a_(a), s_(s), cl_(cooperative_groups::this_cluster()), all_run_(all_run) {
     C_ = int(cl_.num_blocks());
     me_ = int(cl_.block_rank());
     row_ = row;
@@ -199,6 +201,7 @@ class Sampler {
   // logit, off_ logits ahead of it, so that pieces of eight are whole 16-byte
   // loads wherever the row begins.  The slice is [s0_, s1_).
   int C_, me_, row_, off_, s0_, s1_;
+  const bool all_run_;
   const T* g_;
   int turn_ = 0;      // which half of `parts` the next exchange uses
   float max_ = 0.f;
@@ -916,6 +919,8 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
   f.least = least;
   if (lane == 0) s_.warp_first[warp] = f;
   __syncthreads();
+  // The first store to the others' shared memory is below.
+  if (!all_run_) cluster_wait_started();
   // The parts of n members, one in each of n lanes, relative to their common
   // maximum.
   auto join = [&](SaFirst p, int n) {
@@ -1272,11 +1277,17 @@ __global__ void __launch_bounds__(SA_THREADS, MODE == SA_LIST_ONLY ? 2 : 1)
   extern __shared__ __align__(16) uint8_t sa_smem[];
   SaShared& s = *reinterpret_cast<SaShared*>(sa_smem);
   const int n = int(cluster_count_x()), id = int(cluster_id_x());
+  auto cluster = cooperative_groups::this_cluster();
+  // No CTA touches another's shared memory before all of them run.  Arrived
+  // here, waited for only where the first such store is made, so that the wait
+  // lies behind the row's first copies.
+  const bool alone = cluster.num_blocks() == 1;
+  if (!alone) cluster_arrive_started();
   if (MODE != SA_SEARCH_ONLY) {
-    Sampler<T>(a, s, id).template run<MODE>();
+    Sampler<T>(a, s, id, alone).template run<MODE>();
     return;
   }
-  auto cluster = cooperative_groups::this_cluster();
+  if (!alone) cluster_wait_started();
   const int start = int(int64_t(a.B) * id / n), lane = threadIdx.x & 31;
   for (;;) {
     if (cluster.block_rank() == 0 && threadIdx.x < 32) {
@@ -1299,7 +1310,7 @@ __global__ void __launch_bounds__(SA_THREADS, MODE == SA_LIST_ONLY ? 2 : 1)
     cluster.sync();
     const int row = s.row;
     if (row < 0) return;
-    Sampler<T>(a, s, row).template run<MODE>();
+    Sampler<T>(a, s, row, true).template run<MODE>();
     cluster.sync();  // the row's shared memory is done with
   }
 }

@@ -249,3 +249,37 @@ def test_logp_is_the_forward_pass_s():
     cce.cce_forward(H, head, torch.from_numpy(tok).cuda(), logp, lse, ws=ws)
     torch.cuda.synchronize()
     assert np.abs(logp.cpu().numpy() - lp).max() <= 2e-3  # the head's own tolerance
+
+
+def test_clusters_that_start_while_the_gpu_is_busy():
+    """Rows shared by several CTAs, by list and by search, launched again and
+    again beside work that keeps the SMs occupied, so that a cluster's CTAs do
+    not begin at the same time: the tokens of a quiet run."""
+    jobs = []
+    for B, V, dtype in ((10, 20000, F), (3, 70001, BF), (37, 33000, F), (200, 40000, BF)):
+        l = logits(B, B, V, dtype, 2.5 if B < 30 else 1.0, B < 30)
+        s = {k: t32(v, torch.int32 if k == "k" else F) for k, v in settings(V, B).items()}
+        out = [(torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, device="cuda"))
+               for _ in range(2)]
+        jobs.append((l, s, out))
+
+    def launch(stream, which):
+        for l, s, out in jobs:
+            cce.cce_sample_rows(l, s["t"], s["k"], s["p"], s["mp"], s["u"], *out[which], stream)
+
+    launch(None, 0)
+    torch.cuda.synchronize()
+    busy, side = torch.cuda.Stream(), torch.cuda.Stream()
+    a = torch.randn(2048, 2048, device="cuda", dtype=BF)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        with torch.cuda.stream(busy):
+            a @ a
+            a.float().sin_()
+        launch(side, 1)
+        side.synchronize()
+        for _, _, (x, y) in jobs:
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+            y[0].zero_()
+        torch.cuda.current_stream().synchronize()
+    torch.cuda.synchronize()
