@@ -667,6 +667,12 @@ class Sampler {
     const double x = fabsf(d) < 1.f ? sign * double(d) * 0.6931471805599453 : 0.0;
     return 1.0 + x * (1.0 + 0.5 * x);
   }
+  // What sums relative to h are multiplied by to be relative to a larger
+  // maximum's `next`.  c m leaves fp32 only where the next smaller logit is
+  // 2^104 / c below m, so those sums are nothing beside the new maximum.
+  __device__ static double rescale(float h, float next) {
+    return fabsf(h) < INFINITY && fabsf(next) < INFINITY ? double(ex2_approx(h - next)) : 0.0;
+  }
   struct Settings {
     float temp, tp;
     int k;
@@ -858,8 +864,8 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
       // the sums so far, and the instances of the old maximum, in the new scale
       const float nt = bm * CT, nz = bm * cz;
       if (m > -INFINITY) {
-        if (TAIL) tail = (tail + double(ne) * unround(m, CT, ht)) * double(ex2_approx(ht - nt));
-        if (Z) z = bm == INFINITY ? 0.0 : (z + double(ne) * unround(m, cz, hz)) * double(ex2_approx(hz - nz));
+        if (TAIL) tail = (tail + double(ne) * unround(m, CT, ht)) * rescale(ht, nt);
+        if (Z) z = (z + double(ne) * unround(m, cz, hz)) * rescale(hz, nz);
       }
       m = bm;
       ht = nt;
@@ -881,7 +887,8 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
       sum_t += st[k];
       sum_z += sz[k];
     }
-    if (vm == m || sum_t != sum_t || sum_z != sum_z) {  // the maximum itself, NaN, infinities
+    // the maximum itself, NaN, infinities, a maximum whose h is infinite
+    if (vm == m || !(sum_t < INFINITY) || !(sum_z < INFINITY)) {
       sum_t = sum_z = 0.f;
 #pragma unroll
       for (int k = 0; k < NB; ++k)
@@ -892,9 +899,9 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
             ++ne;
             mi = min(mi, cw + p * STEP + k * 256 + lane * 8 + j - off_);
           } else if (l - m > -INFINITY) {
-            const float x = fmaf(l, CT, -ht), y = fmaf(l, cz, -hz);
-            sum_t += ex2_approx(x);
-            sum_z += y == y ? ex2_approx(y) : 0.f;
+            // nothing beside a maximum whose h is not finite (rescale())
+            if (fabsf(ht) < INFINITY) sum_t += ex2_approx(fmaf(l, CT, -ht));
+            if (fabsf(hz) < INFINITY) sum_z += ex2_approx(fmaf(l, cz, -hz));
           }
         }
     }
@@ -1238,6 +1245,8 @@ __device__ void Sampler<T>::run() {
                                       : first_pass<false, true>(float(c_)))
                               : (tail ? first_pass<true, false>(0.f) : first_pass<false, false>(0.f));
   if (same) f.z = f.tail;
+  // a temperature so small that 1 / T is beyond fp32: the mass is not known
+  if (need_z && !(float(c_) < INFINITY)) f.z = INFINITY;
   const bool lead = me_ == 0 && threadIdx.x == 0;
   if (f.hi == 0) {
     if (lead) {

@@ -283,3 +283,75 @@ def test_clusters_that_start_while_the_gpu_is_busy():
             y[0].zero_()
         torch.cuda.current_stream().synchronize()
     torch.cuda.synchronize()
+
+
+LOWEST = {F: [torch.finfo(BF).min, torch.finfo(F).min, -1e38, -1.2e38],
+          BF: [torch.finfo(BF).min, -1e38, -1.2e38]}
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("V", [3000, 20000, 140001])
+def test_two_masks_in_one_row(V, dtype):
+    """Two different very low finite values: their products with log2(e) / T
+    are beyond fp32.  In one lane's piece, one segment, two segments of a warp,
+    two warps, and over whole stretches, ahead of the live logits and among
+    them."""
+    places = [((0,), (1,)), ((0,), (300,)), ((0,), (8192 if V > 9000 else 600,)), ((5,), (520,)),
+              (range(0, 1000), range(1000, 2000)), (range(0, V - 50, 2), range(1, V - 50, 2))]
+    rows = []
+    base = logits(V, 1, V, F, 1.0)[0]
+    for a in LOWEST[dtype]:
+        for b in LOWEST[dtype]:
+            if a == b:
+                continue
+            for pa, pb in places:
+                l = base.clone()
+                l[list(pa)], l[list(pb)] = a, b
+                if pa == (0,):   # nothing live in the first segments
+                    l[:512] = a
+                    l[list(pb)[0]] = b
+                rows.append(l)
+    l = torch.stack(rows).to(dtype)
+    r = np.random.default_rng(V)
+    for i in range(0, l.shape[0], 24):
+        x = l[i:i + 24]
+        n = x.shape[0]
+        for t in (0.0, 0.3, 1.0):
+            for p in (0.5, 0.95, 1.0):
+                check(x, t=[t] * n, p=[p] * n, u=r.random(n).astype(np.float32))
+
+
+def test_logits_whose_products_leave_fp32():
+    """Maxima of either sign beyond 2.36e38 (times T), alone, repeated, rising
+    from segment to segment, and beside infinities."""
+    V = 30000
+    l = torch.zeros(8, V, device="cuda")
+    l[0] = t32(np.linspace(-3.4e38, -2.4e38, V))
+    l[1] = t32(np.linspace(-1.6e38, 1.7e38, V))
+    l[2] = t32(np.linspace(2e38, 3.4e38, V))
+    l[3] = -3e38
+    l[3, ::7] = -3.1e38
+    l[4] = 3e38
+    l[4, ::5] = 2.9e38
+    l[5] = l[1]
+    l[5, [9, 20000]] = float("inf")
+    l[6] = torch.finfo(F).min
+    l[6, 1::2] = torch.finfo(BF).min
+    l[7, 0] = 3.4e38
+    r = np.random.default_rng(8)
+    for t in (0.3, 1.0, 5.0, 1e38):
+        for p in (1.0, 0.9):
+            check(l, t=[t] * 8, p=[p] * 8, u=r.random(8).astype(np.float32))
+
+
+def test_temperatures_whose_inverse_leaves_fp32():
+    """Denormal temperatures with logits of their size, where weights still
+    differ, and of ordinary size, where the maximum is alone."""
+    V = 30000
+    r = np.random.default_rng(12)
+    x = np.stack([np.floor(r.random(V) * 4000) * 2.0 ** -149, r.standard_normal(V),
+                  -np.floor(r.random(V) * 4000) * 2.0 ** -149, np.zeros(V)])
+    l = t32(x)
+    for t in (1e-42, 1e-40, 2e-39):
+        for p in (1.0, 0.9):
+            check(l, t=[t] * 4, p=[p] * 4, u=r.random(4).astype(np.float32))
