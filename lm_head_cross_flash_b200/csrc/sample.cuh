@@ -660,13 +660,15 @@ class Sampler {
   template <bool TAIL, bool Z>
   __device__ SaFirst first_pass(float cz);
   // 2^(c m - h): what a weight of 1 is in sums that are relative to h, or with
-  // sign -1 its inverse.  The difference is a rounding error, so two terms of
-  // the series are enough.
+  // sign -1 its inverse.  The difference is h's rounding error, exact in fp32
+  // and as large as half a step of h: 0.5 where |h| is 2^23.  A logit below m
+  // is at least that far below, so where the difference passes a few hundred
+  // (or h is infinite) the sums are zero, and the bound keeps zero zero.
   __device__ static double unround(float m, float c, float h, double sign = 1.0) {
-    const float d = fmaf(m, c, -h);
-    const double x = fabsf(d) < 1.f ? sign * double(d) * 0.6931471805599453 : 0.0;
-    return 1.0 + x * (1.0 + 0.5 * x);
+    return exp2_fp64(sign * fmin(fmax(double(fmaf(m, c, -h)), -500.0), 500.0));
   }
+  // Rare; not inlined, for the registers.
+  __device__ static __noinline__ double exp2_fp64(double x) { return exp2(x); }
   // What sums relative to h are multiplied by to be relative to a larger
   // maximum's `next`.  c m leaves fp32 only where the next smaller logit is
   // 2^104 / c below m, so those sums are nothing beside the new maximum.

@@ -355,3 +355,38 @@ def test_temperatures_whose_inverse_leaves_fp32():
     for t in (1e-42, 1e-40, 2e-39):
         for p in (1.0, 0.9):
             check(l, t=[t] * 4, p=[p] * 4, u=r.random(4).astype(np.float32))
+
+
+@pytest.mark.parametrize("V", [3000, 140001])
+def test_near_ties_at_the_maximum_of_a_cold_row(V):
+    """Many logits a few steps of fp32 below the maximum, at temperatures where
+    such a step is worth something: max / T is 1e5 to 1e9, and the fp32 product
+    of the two is off by more than the weights differ."""
+    r = np.random.default_rng(V)
+    B = 24
+    x = r.standard_normal((B, V)).astype(np.float32)
+    for b in range(B):
+        top = np.float32(r.uniform(4, 31) * (1 if b % 2 else -1))
+        x[b] = np.minimum(x[b] + min(top, 0) - 8, top - np.float32(1))
+        at = r.choice(V, 300, replace=False)
+        x[b, at] = top - r.integers(0, 40, 300) * np.spacing(np.abs(top))
+    l = t32(x)
+    for t in (1e-4, 1e-5, 3e-6, 1e-6, 1e-7):
+        for p in (1.0, 0.9, 0.35):
+            check(l, t=[t] * B, p=[p] * B, u=r.random(B).astype(np.float32))
+
+
+def test_logp_of_large_logits():
+    """log-softmax at magnitudes where one step of a logit is 0.06 to 8."""
+    r = np.random.default_rng(5)
+    V = 30000
+    rows = []
+    for size in (1e6, 4e6, 1.1e7, 2.5e7, 4e7, 1e8):
+        for sign in (1, -1):
+            top = np.float32(size * r.uniform(0.8, 1.2) * sign)
+            rows.append(top - r.integers(0, 12, V) * np.spacing(np.abs(top)))
+    l = t32(np.stack(rows))
+    n = l.shape[0]
+    for t in (0.0, 1.0, 3.0):
+        check(l, t=[t] * n, u=r.random(n).astype(np.float32))
+        check(l, t=[t] * n, p=[0.6] * n, u=r.random(n).astype(np.float32))
