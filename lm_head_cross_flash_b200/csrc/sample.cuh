@@ -61,10 +61,11 @@ constexpr int SA_CLAIMED = -3;     // and of one that a cluster of the second wo
 enum : int { SA_BOTH = 0, SA_LIST_ONLY = 1, SA_SEARCH_ONLY = 2 };  // what a launch does
 static_assert(SA_CAP == 4 * SA_THREADS && SA_BINS == 4 * SA_THREADS, "four entries per thread");
 
-// Relative error of the pass's sums of exponentials: 2^-22 of ex2.approx, the
-// two roundings of its argument (at most 50 where it counts: 50 ln 2 2^-23),
-// fp32 sums of 8 terms, and a factor with the same errors for each time that a
-// larger maximum turns up.  Together below 8e-6.
+// Relative error of the pass's sums of exponentials: 2^-22 of ex2.approx (once
+// a logit and once in each of two joins, of warps and of CTAs), the roundings
+// of the arguments and of c (3 2^-24 ln 2 times the exponent, at most 50 where
+// it counts) and fp32 sums of 8 terms.  Together below 8e-6, however often a
+// larger maximum turns up: those factors are fp64.
 constexpr double SA_SUM_ERROR = 0x1p-16;
 
 struct SampleArgs {
@@ -671,9 +672,11 @@ class Sampler {
   __device__ static __noinline__ double exp2_fp64(double x) { return exp2(x); }
   // What sums relative to h are multiplied by to be relative to a larger
   // maximum's `next`.  c m leaves fp32 only where the next smaller logit is
-  // 2^104 / c below m, so those sums are nothing beside the new maximum.
+  // 2^104 / c below m, so those sums are nothing beside the new maximum.  In
+  // fp64, since a rising row does this for each of a warp's segments (256 of
+  // ex2.approx's errors of 2^-22 would be four times SA_SUM_ERROR).
   __device__ static double rescale(float h, float next) {
-    return fabsf(h) < INFINITY && fabsf(next) < INFINITY ? double(ex2_approx(h - next)) : 0.0;
+    return fabsf(h) < INFINITY && fabsf(next) < INFINITY ? exp2_fp64(double(h) - double(next)) : 0.0;
   }
   struct Settings {
     float temp, tp;

@@ -390,3 +390,24 @@ def test_logp_of_large_logits():
     for t in (0.0, 1.0, 3.0):
         check(l, t=[t] * n, u=r.random(n).astype(np.float32))
         check(l, t=[t] * n, p=[0.6] * n, u=r.random(n).astype(np.float32))
+
+
+@pytest.mark.parametrize("rise", [2.0, 8.0, 0.3])
+def test_logp_of_rows_that_rise_by_segments(rise):
+    """150 rows of 2^21 logits, one CTA a row, constant over each 512 and
+    rising, so that every segment brings its warp a new maximum (256 times).
+    The rows rise by slightly different steps, each over and over.  logp of the
+    first rank: the sum's terms, three exponentials and their arguments at
+    exponents up to `rise` / ln 2, are off by less than
+    (3 2^-22 + 3 2^-24 rise + 10 2^-24) relative, and so is logp absolutely,
+    with its own half step."""
+    B, V = 150, 1 << 21
+    seg = V // 512
+    step = np.linspace(0.9, 1.1, B)[:, None] * rise / seg
+    x = (step * np.arange(seg)[None]).astype(np.float32)
+    l = t32(x).repeat_interleave(512, 1)
+    _, lp = run(l, t=[0.0] * B, u=[0.5] * B)
+    x = x.astype(np.float64)
+    want = -np.log(512 * np.exp(x - x[:, -1:]).sum(1))
+    tol = 3 * 2.0 ** -22 + (3 * rise * 1.1 + 10) * 2.0 ** -24 + 2.0 ** -24 * np.abs(want)
+    assert (np.abs(lp - want) <= tol).all(), float((np.abs(lp - want) / tol).max())
