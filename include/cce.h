@@ -604,7 +604,7 @@ cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs,
  *   top_p:  of these, the shortest prefix whose mass is at least top_p of
  *           theirs, one rank at least           (top_p >= 1: all)
  *   min_p:  of these, those with w >= min_p     (min_p <= 0: all; the first
- *           rank always stays)
+ *           rank always stays, and above 1 it alone)
  *   token:  the first rank whose running mass exceeds u times the mass of
  *           what stays, 0 <= u < 1 (numbers outside are moved inside)
  * A temperature that is not above 0 takes the first rank.  Several +inf share

@@ -1239,7 +1239,8 @@ __device__ void Sampler<T>::run() {
   o.use_p = o.tp < 1.f;
   o.use_m = mp > 0.f;
   o.thr = o.use_m && mp < 1.f ? double(o.temp) * log(double(mp)) : 0.0;
-  const bool greedy = !(o.temp > 0.f) || o.k == 1;
+  // (a min_p above 1 leaves no weight: the first rank, equal ones apart)
+  const bool greedy = !(o.temp > 0.f) || o.k == 1 || mp > 1.f;
   const bool need_z =
       MODE != SA_SEARCH_ONLY && !greedy && o.k == 0 && (o.use_p || !o.use_m);
   c_ = 1.4426950408889634074 / double(o.temp);

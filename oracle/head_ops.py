@@ -111,7 +111,7 @@ def sample_row(logits, temperature, top_k, top_p, min_p, u):
                 c = np.cumsum(w[:n])
                 n = min(n, max(1, int((c < float(top_p) * c[-1]).sum()) + 1))
             if min_p > 0:
-                n = min(n, max(1, int((w[:n] >= min(float(min_p), 1.0)).sum())))
+                n = min(n, max(1, int((w[:n] >= float(min_p)).sum())))
         c = np.cumsum(w[:n])
         u = min(max(float(u), 0.0), 1.0 - 2.0 ** -24)
         at = order[min(n - 1, int((c <= u * c[-1]).sum()))]

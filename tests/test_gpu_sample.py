@@ -411,3 +411,17 @@ def test_logp_of_rows_that_rise_by_segments(rise):
     want = -np.log(512 * np.exp(x - x[:, -1:]).sum(1))
     tol = 3 * 2.0 ** -22 + (3 * rise * 1.1 + 10) * 2.0 ** -24 + 2.0 ** -24 * np.abs(want)
     assert (np.abs(lp - want) <= tol).all(), float((np.abs(lp - want) / tol).max())
+
+
+@pytest.mark.parametrize("V", [7, 3000, 70001])
+def test_min_p_around_one_with_equal_maxima(V):
+    """min_p = 1 shares the row among the logits at the maximum, above 1 the
+    first of them has it alone, with the other settings in force or not."""
+    l = logits(V, 12, V, F)
+    l[:, [1, 3, V - 1]] = 50.0
+    l[8:, [2, 5]] = float("inf")
+    mp = [1.0, 1.0 + 2.0 ** -23, 2.0, float("inf")] * 3
+    for u in (0.1, 0.5, 0.9):
+        tok = check(l, mp=mp, u=[u] * 12)
+        assert all(tok[r] == (1 if r < 8 else 2) for r in range(12) if mp[r] > 1)
+        check(l, mp=mp, t=[0.5] * 12, k=[20] * 12, p=[0.9] * 12, u=[u] * 12)

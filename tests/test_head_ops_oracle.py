@@ -149,3 +149,12 @@ def test_binding_refuses_what_the_library_would_misread():
     with pytest.raises(ValueError, match="CUDA"):
         cce.cce_norm_backward(cpu, cpu, cpu, cpu, cpu, cpu)
     assert cce.fp8_groups(1) == 1 and cce.fp8_groups(128) == 1 and cce.fp8_groups(129) == 2
+
+
+def test_min_p_above_one_leaves_the_first_rank():
+    """Of several logits at the maximum too: w = 1 is not at least min_p."""
+    l = [0.0, 2.0, 2.0, 1.0, 2.0]
+    assert O.sample_row(l, 1, 0, 1, 1.0, 0.9)[2].tolist() == [1, 2, 4]
+    for mp in (1.0 + 2.0 ** -23, 5.0, np.inf):
+        assert O.sample_row(l, 1, 0, 1, mp, 0.9)[2].tolist() == [1]
+    assert O.sample_row([1.0, np.inf, np.inf], 1, 0, 1, 2.0, 0.9)[0] == 1
