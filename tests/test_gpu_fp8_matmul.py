@@ -119,3 +119,28 @@ def test_rounds_once_and_repeats_its_bits(ws):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, c32)
+
+
+@pytest.mark.parametrize("M,N,K", [(100, 9500, 8192), (100, 9500, 8193), (128, 9500, 8320),
+                                   (65, 20000, 8321), (33, 9500, 16385), (100, 2600, 33000)])
+def test_few_rows_whose_scales_do_not_fit(M, N, K, ws):
+    """The few-rows kernel keeps a CTA's scales in shared memory, 8,192 of
+    them: M padded to 16, 32, 64 or 128, times the groups of K that a CTA takes
+    (all of them where the head has 75 tiles of 128 rows or more, else a share
+    of 1/2, 1/4 or 1/8).  Just below that (the first case) it runs; with one
+    group more, up to 128 rows go to the many-rows kernel, whose tiles are
+    taller than the operand."""
+    G, tiles = O.groups(K), O.groups(N)
+    split = 1
+    while split < 8 and 2 * split * tiles <= 148 and 2 * split <= G:
+        split *= 2
+    scales = (64 if M <= 64 else 128) * -(-G // split)
+    assert (scales <= 8192) == ((M, K) == (100, 8192))
+    a, sa, av = operand(11, M, K, "rows")
+    b, sb, bv = operand(12, N, K, "blocks")
+    for ct in ("f32", "bf16"):
+        big = torch.full((M + 1, N + 3), 7.0, dtype=T[ct], device="cuda")
+        cce.cce_fp8_matmul(a, sa, b, sb, big[:M, :N], ws)
+        assert cce.cce_device_status(ws) == 0
+        check(big[:M, :N], av, bv, K, HALF[ct])
+        assert (big[:M, N:] == 7.0).all() and (big[M:] == 7.0).all()
