@@ -551,7 +551,9 @@ cce_status cce_fp8_quant_blocks(const void* W, cce_dtype w_dtype, int64_t N,
  * is made on the tensor cores; the scales are applied in fp32.
  * A and B: 16-byte aligned, lda and ldb multiples of 16 (bytes; not looked at
  * for a single row).  K <= 65,536.  The first 256 bytes of ws hold the status
- * word (zeroed once before first use); no more is used.
+ * word (zeroed once before first use); no more is used.  CCE_ERR_UNSUPPORTED
+ * for valid sizes above 128 rows means that the library was compiled with flags
+ * under which the kernel's register hand-over does not add up.
  */
 cce_status cce_fp8_matmul(const uint8_t* A, int64_t lda, const float* SA,
                           const uint8_t* B, int64_t ldb, const float* SB,

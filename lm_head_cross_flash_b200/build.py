@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -47,6 +48,21 @@ def needs_build() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+# Kernels that hand registers from some warps to others (setmaxnreg): the sum
+# is counted against this many a thread at launch, and the library refuses to
+# run such a kernel when it was compiled to another number.
+REGISTERS = {"fp8_rows_kernel": 168}
+
+
+def check_registers(ptxas_log: str) -> None:
+    """Raise RuntimeError unless ptxas -v reports REGISTERS."""
+    for kernel, want in REGISTERS.items():
+        got = re.findall(r"entry function '\w*" + kernel + r"\w*'(?:.*\n)+?.*Used (\d+) registers",
+                         ptxas_log)
+        if [int(n) for n in got] != [want]:
+            raise RuntimeError(f"{kernel}: compiled to {got} registers, its hand-over needs {want}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
@@ -58,6 +74,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         f.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stderr[-4000:]}")
+    check_registers(r.stdout + r.stderr)
     os.replace(LIB + ".tmp", LIB)
     if verbose:
         print(r.stderr)

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "fp8_mm.cuh"
+#include "kept.cuh"
 #include "row_ops.cuh"
 #include "sample.cuh"
 
@@ -417,12 +418,23 @@ cce_status cce_fp8_matmul(const uint8_t* A, int64_t lda, const float* SA, const 
   static bool done[64];
   s = set_smem_once(fp8_rows_kernel, F8_SMEM, done);
   if (s != CCE_OK) return s;
-  // the kernel's register hand-over counts on what it is launched with
-  static const int regs = [] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, fp8_rows_kernel) == cudaSuccess ? fa.numRegs : 0;
-  }();
-  if (regs != F8_REGS) return CCE_ERR_CUDA;
+  // The kernel's register hand-over waits for ever if it was compiled to fewer
+  // registers than it counts on; the build checks the same.
+  static Kept kept_regs;
+  int regs = 0;
+  if (!kept_regs.get(
+          [](int* n) {
+            cudaFuncAttributes fa;
+            if (cudaFuncGetAttributes(&fa, fp8_rows_kernel) != cudaSuccess) {
+              cudaGetLastError();
+              return false;
+            }
+            *n = fa.numRegs;
+            return true;
+          },
+          &regs))
+    return CCE_ERR_CUDA;
+  if (regs != F8_REGS) return CCE_ERR_UNSUPPORTED;
   a.n_rt = int(ceil_div(M, 2 * F8_BM));
   a.n_ct = int(ceil_div(N, F8_BN));
   // row tiles of one raster group: 48 MB of A, so that a group stays in L2

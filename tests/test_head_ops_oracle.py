@@ -2,6 +2,7 @@
 need no GPU."""
 
 import ctypes
+import subprocess
 
 import numpy as np
 import pytest
@@ -158,3 +159,36 @@ def test_min_p_above_one_leaves_the_first_rank():
     for mp in (1.0 + 2.0 ** -23, 5.0, np.inf):
         assert O.sample_row(l, 1, 0, 1, mp, 0.9)[2].tolist() == [1]
     assert O.sample_row([1.0, np.inf, np.inf], 1, 0, 1, 2.0, 0.9)[0] == 1
+
+
+def test_build_checks_the_registers_of_the_hand_over():
+    line = ("ptxas info    : Compiling entry function '_ZN3cce15fp8_rows_kernelE14CUtensorMap_stS0_NS_"
+            "7Fp8ArgsE' for 'sm_100a'\nptxas info    : Function properties for x\n    0 bytes stack "
+            "frame\nptxas info    : Used %d registers, used 16 barriers\n"
+            "ptxas info    : Compiling entry function 'y' for 'sm_100a'\n"
+            "ptxas info    : Used 168 registers\n")
+    build.check_registers(line % 168)
+    for bad in (line % 128, line % 255, "", line.replace("fp8_rows", "fp8_few") % 168):
+        with pytest.raises(RuntimeError, match="fp8_rows_kernel"):
+            build.check_registers(bad)
+
+
+def test_a_failed_query_is_asked_again(tmp_path):
+    """What the driver says of a kernel is kept from the first success on."""
+    src = tmp_path / "kept.cpp"
+    src.write_text("""
+#include "kept.cuh"
+int main() {
+  static cce::Kept k;
+  int asked = 0, v = 0;
+  auto fail = [&](int*) { ++asked; return false; };
+  auto give = [&](int* n) { ++asked; *n = 168; return true; };
+  if (k.get(fail, &v) || k.get(fail, &v) || asked != 2) return 1;
+  if (!k.get(give, &v) || v != 168 || asked != 3) return 2;
+  v = 0;
+  return k.get(fail, &v) && v == 168 && asked == 3 ? 0 : 3;
+}
+""")
+    exe = tmp_path / "kept"
+    subprocess.run(["g++", "-std=c++17", "-x", "c++", "-I", build.SRC, "-o", str(exe), str(src)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
