@@ -774,13 +774,15 @@ def orpo_norm_head_pass(X, norm_w, eps, head: Head, labels, layout, lam, sft_sco
     """``orpo_head_pass`` from the residual stream X [M, D] on: the final norm
     with its 8-bit checkpoint, the head's pass, and the norm's gradient from
     the checkpoint (``norm.dX``, ``norm.dW``).  X is read by the first kernel
-    only; its memory may be reused once that has run."""
-    cce_norm_forward(X, norm_w, eps, H=norm.H, X8=norm.X8, Xs=norm.Xs, rstd=norm.rstd,
-                     stream=stream)
-    orpo_head_pass(norm.H, head, labels, layout, lam, sft_scope, filter_eps, block_skip, buf,
-                   stream)
-    cce_norm_backward(norm.X8, norm.Xs, norm.rstd, norm_w, buf.dH, norm.dX, norm.dW, norm.ws,
-                      stream)
+    only; its memory may be reused once that has run.  The whole pass is made
+    on X's device and, without ``stream``, on that device's current stream."""
+    with torch.cuda.device(X.device):  # the head's own calls go to the current device
+        cce_norm_forward(X, norm_w, eps, H=norm.H, X8=norm.X8, Xs=norm.Xs, rstd=norm.rstd,
+                         stream=stream)
+        orpo_head_pass(norm.H, head, labels, layout, lam, sft_scope, filter_eps, block_skip, buf,
+                       stream)
+        cce_norm_backward(norm.X8, norm.Xs, norm.rstd, norm_w, buf.dH, norm.dX, norm.dW, norm.ws,
+                          stream)
 
 
 @dataclass

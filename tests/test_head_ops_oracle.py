@@ -192,3 +192,32 @@ int main() {
     exe = tmp_path / "kept"
     subprocess.run(["g++", "-std=c++17", "-x", "c++", "-I", build.SRC, "-o", str(exe), str(src)], check=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_the_norm_and_head_pass_stays_on_one_device(monkeypatch):
+    """The head's calls go to the current device and its stream, the norm's to
+    the tensors': all three are made with the tensors' device current."""
+    now, seen = [torch.device("cuda:0")], []
+
+    class Current:
+        def __init__(self, device):
+            self.device = torch.device(device)
+
+        def __enter__(self):
+            now.append(self.device)
+
+        def __exit__(self, *_):
+            now.pop()
+
+    class Any:
+        device = torch.device("cuda:1")
+
+        def __getattr__(self, name):
+            return None
+
+    monkeypatch.setattr(torch.cuda, "device", Current)
+    for f in ("cce_norm_forward", "orpo_head_pass", "cce_norm_backward"):
+        monkeypatch.setattr(cce, f, lambda *a, f=f, **k: seen.append((f, now[-1].index)))
+    cce.orpo_norm_head_pass(Any(), None, 1e-6, None, None, None, 0.1, "full", 0.0, False, Any(), Any())
+    assert seen == [("cce_norm_forward", 1), ("orpo_head_pass", 1), ("cce_norm_backward", 1)]
+    assert len(now) == 1
