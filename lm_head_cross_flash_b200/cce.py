@@ -795,10 +795,19 @@ class Fp8Head:
 
     @staticmethod
     def from_dense(w, stream=None):
+        """The 8-bit form of ``w`` [V, D], made on ``stream`` behind what the
+        current stream has been given so far (``w`` may be its work, and the
+        new tensors' memory may still be in use there)."""
         V, D = w.shape
         h = Fp8Head(fp8_empty(V, D, w.device),
                     torch.empty(fp8_groups(V), fp8_groups(D), dtype=torch.float32,
                                 device=w.device))
+        if stream is not None:
+            now = torch.cuda.current_stream(w.device)
+            if stream != now:
+                stream.wait_stream(now)
+                h.q.record_stream(stream)
+                h.s.record_stream(stream)
         cce_fp8_quant_blocks(w, h.q, h.s, stream)
         return h
 

@@ -253,3 +253,29 @@ def test_rows_far_apart():
     cce.cce_fp8_matmul(a8, sa, hb.q, hb.s, dense, st)
     cce.cce_fp8_matmul(a8, sa, hb.q, hb.s, wide, st)
     assert torch.equal(dense, wide)
+
+
+def test_a_head_made_on_another_stream():
+    """The codes' memory may still be written by the current stream's earlier
+    work (a tensor freed behind it), and so may the dense head: a head made on
+    another stream comes behind both."""
+    V, D = 4096, 512
+    _, _, W, _ = make(9, 1, D, V)
+    want = cce.Fp8Head.from_dense(W)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    late = torch.zeros_like(W)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        q, s = torch.empty(V, D, dtype=torch.uint8, device="cuda"), torch.empty(V // 128, D // 128, device="cuda")
+        torch.cuda._sleep(20_000_000)  # some 10 ms
+        q.fill_(0x11)
+        s.fill_(3.0)
+        late.copy_(W)
+        del q, s
+        got = cce.Fp8Head.from_dense(late, stream=side)
+        side.synchronize()
+        assert torch.equal(got.q.view(torch.uint8), want.q.view(torch.uint8)) and torch.equal(got.s, want.s)
+        torch.cuda.synchronize()
+        late.zero_()
+        del got
