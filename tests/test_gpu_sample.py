@@ -425,3 +425,25 @@ def test_min_p_around_one_with_equal_maxima(V):
         tok = check(l, mp=mp, u=[u] * 12)
         assert all(tok[r] == (1 if r < 8 else 2) for r in range(12) if mp[r] > 1)
         check(l, mp=mp, t=[0.5] * 12, k=[20] * 12, p=[0.9] * 12, u=[u] * 12)
+
+
+@pytest.mark.parametrize("B,V,share", [(5001, 2100, 1.0), (4099, 3000, 0.1), (2048, 9000, 0.5), (40, 40000, 1.0)])
+def test_searched_rows_spread_over_a_large_batch(B, V, share):
+    """Flat rows (searched) at random places among sharp ones: each gets its
+    token once, whichever cluster takes it."""
+    r = np.random.default_rng(B)
+    flat = r.random(B) < share
+    x = np.where(flat[:, None], 0.01, 6.0) * r.standard_normal((B, V))
+    l = t32(x)
+    u = r.random(B).astype(np.float32)
+    check(l, p=[0.9] * B, u=u)
+
+
+def test_a_million_rows():
+    """More rows than the search goes over in a step, none of them left to it."""
+    B, V = (1 << 20) + 77, 8
+    l = torch.randn(B, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    tok, lp = run(l, t=np.zeros(B), u=np.full(B, 0.5))
+    assert np.array_equal(tok, l.argmax(1).cpu().numpy())
+    want = torch.log_softmax(l.double(), 1).amax(1).cpu().numpy()
+    assert (np.abs(lp - want) <= 7e-6 + 2.0 ** -24 * np.abs(want)).all()
