@@ -587,7 +587,8 @@ cce_status cce_norm_forward(const void* X, cce_dtype x_dtype, int64_t M,
  * dH: [M, D], f32 or bf16 (the dH of cce_backward_dh).  dX: [M, D], f32 or
  * bf16, overwritten.  dW: fp32 [D], overwritten, or NULL (a frozen norm; ws
  * may then be NULL).  rstd is taken as given (the forward's, from the exact
- * X).  Sums in fp32, in an order that depends on the sizes alone.
+ * X).  Sums in fp32, in an order that depends on the sizes and on whether all
+ * rows are aligned (16 bytes, 8 for codes, and D a multiple of 8).
  * ws: cce_norm_backward_workspace_bytes(M, D) bytes (0: invalid sizes).
  */
 size_t cce_norm_backward_workspace_bytes(int64_t M, int64_t D);

@@ -81,10 +81,11 @@ void with_team(int64_t D, F f) {
   f(Int<512>(), Int<4>());
 }
 
-// Blocks of the norm's kernels: what runs at once.
+// Blocks of the norm's kernels, for aligned rows or not: what runs at once.
+template <bool VEC>
 int norm_blocks(int64_t M, int64_t D) {
   int64_t rpb = 1, per_sm = 1;
-  with_team<true>(D, [&](auto tpr, auto r) {
+  with_team<VEC>(D, [&](auto tpr, auto r) {
     rpb = norm_block(tpr()) / tpr();
     per_sm = norm_per_sm(tpr(), r());
   });
@@ -299,7 +300,7 @@ cce_status cce_norm_forward(const void* X, cce_dtype x_dtype, int64_t M, int64_t
           constexpr int T = decltype(tpr)::value, B = norm_block(T);
           norm_fwd_kernel<decltype(v)::value, typename decltype(tx)::type,
                           typename decltype(th)::type, T, decltype(r)::value>
-              <<<norm_blocks(M, D), B, 0, st>>>(a);
+              <<<norm_blocks<decltype(v)::value>(M, D), B, 0, st>>>(a);
         });
       });
     });
@@ -309,7 +310,9 @@ cce_status cce_norm_forward(const void* X, cce_dtype x_dtype, int64_t M, int64_t
 
 size_t cce_norm_backward_workspace_bytes(int64_t M, int64_t D) {
   if (M <= 0 || D <= 0 || M > kMaxRows || D > kMaxNormD) return 0;
-  return kStatusBytes + size_t(norm_blocks(M, D)) * size_t(D) * 4;
+  // one part of dW for each block, of whichever form the rows' alignment asks for
+  return kStatusBytes + size_t(std::max(norm_blocks<true>(M, D), norm_blocks<false>(M, D))) *
+                            size_t(D) * 4;
 }
 
 cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs, const float* rstd,
@@ -346,7 +349,7 @@ cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs, c
                    codes8(X8, ldx8);
   if (dW != nullptr)
     a.dw_part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes);
-  const int grid = norm_blocks(M, D);
+  const int grid = vec ? norm_blocks<true>(M, D) : norm_blocks<false>(M, D);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   ProfScope ps(PK_NORM, st);
   with_type(dx_dtype, [&](auto tx) {

@@ -221,3 +221,11 @@ def test_the_norm_and_head_pass_stays_on_one_device(monkeypatch):
     cce.orpo_norm_head_pass(Any(), None, 1e-6, None, None, None, 0.1, "full", 0.0, False, Any(), Any())
     assert seen == [("cce_norm_forward", 1), ("orpo_head_pass", 1), ("cce_norm_backward", 1)]
     assert len(now) == 1
+
+
+def test_the_norm_s_workspace_holds_a_part_for_each_block(lib):
+    """Rows that are not aligned, 257 to 1,024 wide, are taken one by a block:
+    as many blocks as rows, up to four on each of 148 SMs (no GPU: the count
+    that the library then takes)."""
+    for M, D in ((300, 500), (300, 1000), (100, 257), (592, 1023)):
+        assert lib.cce_norm_backward_workspace_bytes(M, D) >= 256 + M * D * 4
