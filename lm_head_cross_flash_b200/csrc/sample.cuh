@@ -300,12 +300,10 @@ class Sampler {
   __device__ float below(float l) const { return l == max_ ? 0.f : max_ - l; }
   __device__ int bin_of(float l) const { return bin_below(max_, l, bin_scale_); }
 
-  // round(2^bits * 2^x) for x <= 0: with k = round(32 x), r = x - k/32,
+  // 2^(x + places), |x| up to 900: with k = round(32 x), r = x - k/32,
   // 2^x = 2^(k div 32) 2^((k mod 32)/32) 2^r, and 2^r by its series to r^5
-  // (the next term is below 2.3e-15).  The last addition leaves the integer
-  // in the low bits of the sum.
-  __device__ u64 weight_log2(double x) const {
-    if (!(x > -50.0)) return 0;
+  // (the next term is below 2.3e-15).
+  __device__ double exp2_fp64(double x, int places = 0) const {
     constexpr double MAGIC = 6755399441055744.0;  // 1.5 * 2^52
     const double kd = fma(x, 32.0, MAGIC);
     const int k = __double2loint(kd);
@@ -316,9 +314,15 @@ class Sampler {
     p = fma(r, p, L * L / 2.0);
     p = fma(r, p, L);
     const double t = s_.pow2[k & 31];
-    const double ts = __hiloint2double(__double2hiint(t) + ((k >> 5) + a_.bits) * (1 << 20),
+    const double ts = __hiloint2double(__double2hiint(t) + ((k >> 5) + places) * (1 << 20),
                                        __double2loint(t));
-    const double w = fma(ts, r * p, ts) + 4503599627370496.0;  // + 2^52
+    return fma(ts, r * p, ts);
+  }
+  // round(2^bits * 2^x) for x <= 0.  The addition leaves the integer in the low
+  // bits of the sum.
+  __device__ u64 weight_log2(double x) const {
+    if (!(x > -50.0)) return 0;
+    const double w = exp2_fp64(x, a_.bits) + 4503599627370496.0;  // + 2^52
     return u64(__double_as_longlong(w)) & 0x000FFFFFFFFFFFFFull;
   }
   __device__ u64 weight(float l) const {
@@ -666,18 +670,17 @@ class Sampler {
   // and as large as half a step of h: 0.5 where |h| is 2^23.  A logit below m
   // is at least that far below, so where the difference passes a few hundred
   // (or h is infinite) the sums are zero, and the bound keeps zero zero.
-  __device__ static double unround(float m, float c, float h, double sign = 1.0) {
-    return exp2_fp64(sign * fmin(fmax(double(fmaf(m, c, -h)), -500.0), 500.0));
+  __device__ double unround(float m, float c, float h, float sign = 1.f) const {
+    return exp2_fp64(double(sign * fminf(fmaxf(fmaf(m, c, -h), -500.f), 500.f)));
   }
-  // Rare; not inlined, for the registers.
-  __device__ static __noinline__ double exp2_fp64(double x) { return exp2(x); }
   // What sums relative to h are multiplied by to be relative to a larger
   // maximum's `next`.  c m leaves fp32 only where the next smaller logit is
   // 2^104 / c below m, so those sums are nothing beside the new maximum.  In
   // fp64, since a rising row does this for each of a warp's segments (256 of
   // ex2.approx's errors of 2^-22 would be four times SA_SUM_ERROR).
-  __device__ static double rescale(float h, float next) {
-    return fabsf(h) < INFINITY && fabsf(next) < INFINITY ? exp2_fp64(double(h) - double(next)) : 0.0;
+  __device__ double rescale(float h, float next) const {
+    return fabsf(h) < INFINITY && fabsf(next) < INFINITY
+               ? exp2_fp64(fmax(double(h) - double(next), -900.0)) : 0.0;
   }
   struct Settings {
     float temp, tp;
@@ -914,8 +917,8 @@ __device__ SaFirst Sampler<T>::first_pass(float cz) {
     if (TAIL) tail += double(sum_t);
     if (Z) z += double(sum_z);
   }
-  if (TAIL) tail *= unround(m, CT, ht, -1.0);
-  if (Z) z *= unround(m, cz, hz, -1.0);
+  if (TAIL) tail *= unround(m, CT, ht, -1.f);
+  if (Z) z *= unround(m, cz, hz, -1.f);
   // threads -> CTA
   SaFirst f;
   f.hi = mi != 0x7FFFFFFF ? rank_of(m, mi) : 0;
