@@ -677,10 +677,11 @@ class Sampler {
   // maximum's `next`.  c m leaves fp32 only where the next smaller logit is
   // 2^104 / c below m, so those sums are nothing beside the new maximum.  In
   // fp64, since a rising row does this for each of a warp's segments (256 of
-  // ex2.approx's errors of 2^-22 would be four times SA_SUM_ERROR).
+  // ex2.approx's errors of 2^-22 would be four times SA_SUM_ERROR).  Nothing
+  // too where the maxima are 2^-900 apart, which keeps a bounded unround() out.
   __device__ double rescale(float h, float next) const {
-    return fabsf(h) < INFINITY && fabsf(next) < INFINITY
-               ? exp2_fp64(fmax(double(h) - double(next), -900.0)) : 0.0;
+    const double x = double(h) - double(next);  // NaN, if both are infinite
+    return x > -900.0 && fabsf(h) < INFINITY ? exp2_fp64(x) : 0.0;
   }
   struct Settings {
     float temp, tp;

@@ -447,3 +447,21 @@ def test_a_million_rows():
     assert np.array_equal(tok, l.argmax(1).cpu().numpy())
     want = torch.log_softmax(l.double(), 1).amax(1).cpu().numpy()
     assert (np.abs(lp - want) <= 7e-6 + 2.0 ** -24 * np.abs(want)).all()
+
+
+def test_maxima_that_rise_by_more_than_weights_hold():
+    """Each of a warp's segments outdoes the last one's maximum by 2^100 to
+    2^(10^27), at magnitudes where the products with log2(e) / T are rounded by
+    as much, up or down."""
+    r = np.random.default_rng(14)
+    V = 300001
+    seg = np.arange(V) // 512
+    rise = np.sort(r.random((8, V)), 1)
+    rows = [1e30 + 1e24 * seg, -1e30 + 1e24 * seg, 1e12 + 1e6 * seg, 100.0 * seg, 1e6 + 0.0625 * seg,
+            1e20 * (1 + seg % 7), 1e9 * r.standard_normal(V)]
+    rows += [c * (1 + x * 2.0 ** -14) for c, x in zip((1e30, -1e30, 2e25, 3e20, -7e15, 1e11, 5e8, 1e36), rise)]
+    l = t32(np.stack(rows))
+    n = l.shape[0]
+    for t in (0.0, 1.0, 8.7e-7):
+        for p in (1.0, 0.3):
+            check(l, t=[t] * n, p=[p] * n, u=r.random(n).astype(np.float32))
