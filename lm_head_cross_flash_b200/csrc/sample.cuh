@@ -325,9 +325,11 @@ class Sampler {
     const double w = exp2_fp64(x, a_.bits) + 4503599627370496.0;  // + 2^52
     return u64(__double_as_longlong(w)) & 0x000FFFFFFFFFFFFFull;
   }
+  // l - max, exact (infinities are equal).
+  __device__ double diff(float l) const { return l == max_ ? 0.0 : double(l) - double(max_); }
   __device__ u64 weight(float l) const {
     if (l == max_) return u64(1) << a_.bits;
-    return weight_log2((double(l) - double(max_)) * c_);
+    return weight_log2(diff(l) * c_);
   }
 
   // ------------------------------------------------- block and cluster --
@@ -690,7 +692,7 @@ class Sampler {
     double u, thr;  // min_p as a bound on l - max
   };
   __device__ bool above_min(float l, const Settings& o) const {
-    return (l == max_ ? 0.0 : double(l) - double(max_)) >= o.thr;
+    return diff(l) >= o.thr;
   }
   __device__ static u64 nucleus(float tp, double z) {  // ceil(tp z), one at least
     return u64(fmax(1.0, ceil(double(tp) * z)));
@@ -1283,7 +1285,7 @@ __device__ void Sampler<T>::run() {
     a_.token[row_] = rank_index(token);
     if (a_.logp != nullptr)
       a_.logp[row_] =
-          float(-double(below(rank_value(token))) - log1p(f.tail + double(f.n - 1)));
+          float(diff(rank_value(token)) - log1p(f.tail + double(f.n - 1)));
   }
 }
 

@@ -465,3 +465,13 @@ def test_maxima_that_rise_by_more_than_weights_hold():
     for t in (0.0, 1.0, 8.7e-7):
         for p in (1.0, 0.3):
             check(l, t=[t] * n, p=[p] * n, u=r.random(n).astype(np.float32))
+
+
+def test_logp_far_below_the_maximum_is_rounded_once():
+    """Hot rows that take tokens hundreds below the maximum: logp is off by half
+    a step, not by another half for the difference."""
+    r = np.random.default_rng(15)
+    B, V = 64, 20000
+    l = t32(-2000 * r.random((B, V)) + r.random((B, 1)) * 50)
+    for t in (300.0, 2000.0, 1e30):
+        check(l, t=[t] * B, u=r.random(B).astype(np.float32))
