@@ -550,10 +550,12 @@ cce_status cce_fp8_quant_blocks(const void* W, cce_dtype w_dtype, int64_t N,
  * C: [M, N], f32 or bf16, summed in fp32 and rounded once.  Every group's sum
  * is made on the tensor cores; the scales are applied in fp32.
  * A and B: 16-byte aligned, lda and ldb multiples of 16 (bytes; not looked at
- * for a single row).  K <= 65,536.  The first 256 bytes of ws hold the status
- * word (zeroed once before first use); no more is used.  CCE_ERR_UNSUPPORTED
- * for valid sizes above 128 rows means that the library was compiled with flags
- * under which the kernel's register hand-over does not add up.
+ * for a single row).  K <= 65,536.  A group's two scales are multiplied in fp32
+ * first: below 2^-126 the product loses digits, from 2^128 on it is infinite.
+ * The first 256 bytes of ws hold the status word (zeroed once before first
+ * use); no more is used.  CCE_ERR_UNSUPPORTED for sizes within these limits
+ * means that the library was compiled with flags under which the many-rows
+ * kernel's register hand-over does not add up.
  */
 cce_status cce_fp8_matmul(const uint8_t* A, int64_t lda, const float* SA,
                           const uint8_t* B, int64_t ldb, const float* SB,
@@ -564,7 +566,9 @@ cce_status cce_fp8_matmul(const uint8_t* A, int64_t lda, const float* SA,
 /*
  * Final norm, the step that makes the head's rows from the residual stream:
  *   rstd[m] = 1 / sqrt(mean_d X[m,d]^2 + eps),  H[m,d] = X[m,d] rstd[m] w[d]
- * X: [M, D], f32 or bf16, D <= 16,384; w: [D], f32 or bf16.  Computed in fp32.
+ * X: [M, D], f32 or bf16, D <= 16,384; w: [D], f32 or bf16.  Computed in fp32,
+ * the sum of squares too: from 2^128 on (elements of some 1e19 / sqrt(D)) it is
+ * infinite and rstd is 0.
  * Outputs, each optional, at least one:
  *   H: [M, D], f32 or bf16 (the H of cce_forward);
  *   H8, Hs: the rows of H in 8 bits, made from the fp32 values (the A of
@@ -615,7 +619,8 @@ cce_status cce_norm_backward(const uint8_t* X8, int64_t ldx8, const float* Xs,
  * temperature, top_p, min_p, u: fp32 [B]; top_k: int32 [B]; all but u may be
  * NULL (1, all, all, all).  tokens: int32 [B].  logp: fp32 [B] or NULL, the
  * token's log-softmax over all live logits at temperature 1, which is
- * cce_forward's logp for that label (0 for token -1).
+ * cce_forward's logp for that label (0 for token -1); the sum behind it is of
+ * fp32 exponentials and within 8e-6 of its value.
  * Masses are sums of fixed-point numbers (weights in fp64, rounded to
  * 2^-45, for V above 2^18 to 2^-(63 - ceil(log2 V))), so the tokens do not
  * depend on the order of summation.  One or two kernels, no workspace; until

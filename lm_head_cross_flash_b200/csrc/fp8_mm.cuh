@@ -102,8 +102,9 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, uint32_t mask, uint
 // What bounds it (2048 x 18944 x 4096, codes and scales constant): 135 us in
 // all, 105 with the partials left alone, 105 with the MMAs left out, so each
 // side is near the other's time and the hand-over between them is what is
-// left.  Measured against this form: fma.rn.f32 instead of f32x2 1255 us (2048
-// x 128256 x 4096, 1013 here), tiles of 256 x 128 with four accumulators 1343,
+// left.  With real codes and scales 177 us in a long run, at 1.47 GHz under the
+// power cap.  2048 x 128256 x 4096: 1013 us cold, 1190 in a long run.  Measured
+// against this form when it took 1013: fma.rn.f32 instead of f32x2 1255 us, tiles of 256 x 128 with four accumulators 1343,
 // halves of 128 columns with accumulators of their own 1148, sixteen draining
 // warps 1614 (the instructions that are not FMAs add up).
 constexpr int F8_BM = 128, F8_BN = 256, F8_BK = 128;
@@ -409,8 +410,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 // NP: rows of a, padded (16, 32, 64, 128).  A stage holds 128 rows of b and
 // the NP rows of a for one group; four accumulators of NP columns.  N = 128256,
 // K = 4096: 87.5 us with one row (6.0 TB/s, 91 % of the measured copy rate),
-// 114 us with 64; N = 73440, K = 1536 to fp32: 24 us with 16 rows, 29 us with
-// 61.  More stages (8 to 12 instead of 6 to 8) changed nothing.
+// 114 to 125 us with 64, 160 with 128; N = 73440, K = 1536 to fp32: 24 us with 16
+// rows, 29 us with 61, 42 with 128.  The form for 128 rows spills 64 bytes a
+// thread (64 sums and as many partials in 168 registers), the others none.
+// More stages (8 to 12 instead of 6 to 8) changed nothing.
 constexpr int FF_MAX_SCALES = 8192;  // NP * groups per CTA, kept in shared memory
 template <int NP>
 struct FfCfg {

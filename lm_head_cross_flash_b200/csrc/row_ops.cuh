@@ -334,7 +334,7 @@ constexpr int norm_per_sm(int tpr, int r) {
 // once; the codes of x and of h come from the same registers.  A block takes
 // row after row, the next one on its way while the current one is summed.
 // [8192, 2048] bf16 to H and checkpoint 19 us (4.4 TB/s), [32768, 4096] 135 us
-// (5.0 TB/s); bound by its instructions, 210 a warp and 256 elements (with
+// (5.0 TB/s); bound by its instructions, 213 a warp and 256 elements (with
 // IEEE quotients in every thread and the weights read again for each row, 273
 // and 162 us).
 template <bool VEC, typename T, typename TH, int TPR, int R>
@@ -419,7 +419,11 @@ struct NormBwdArgs {
 // norm_dw_kernel, so dw does not depend on timing.
 // The next row's loads are issued before the current row's sum.  [32768, 4096]
 // with fp32 dH 157 us (6.0 TB/s, 92 % of the measured copy rate); 244 us while
-// its registers let one block of 512 threads onto an SM instead of two.
+// its registers let one block of 512 threads onto an SM instead of two.  Rows
+// wider than 8,192 take four pieces a thread, whose weights, dw terms and next
+// row do not fit 128 registers: 304 to 856 bytes of spills a thread, [4096,
+// 16384] 232 us (2.0 TB/s; [4096, 8192] 45 us, 5.3 TB/s), 350 where rows are not
+// aligned.
 template <bool VEC, typename TX, typename TH, int TPR, int R>
 __global__ void __launch_bounds__(norm_block(TPR), norm_per_sm(TPR, R))
     norm_bwd_kernel(const __grid_constant__ NormBwdArgs a) {

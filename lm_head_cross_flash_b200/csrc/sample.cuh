@@ -30,13 +30,14 @@
 //    list takes is binned again, over its values or, where those are all
 //    equal, over its indices.  A step that does not halve it is followed by a
 //    bisection, so the search ends for every input.
-// Measured: one row of 73,440 fp32 logits 10.4 us; 256 rows of 262,144 bf16 45
-// us greedy with logp (20 us of DRAM; 12 instructions a logit), 62 us with
-// top-k 50, 277 us with top-p 0.95 where a fifth of the rows is flat, 657 us
-// where all are.
+// Measured: one row of 73,440 fp32 logits 10.6 us by list and 59 by search; 256
+// rows of 262,144 bf16 46 us greedy with logp (20 us of DRAM; 12 instructions a
+// logit), 62 us with top-k 50, 262 us with top-p 0.95 where a fifth of the rows
+// is flat, 652 us where all are, but for some likely tokens, 752 without those.
 // Many rows run as two launches: the list with few CTAs a row (its fixed
-// costs, mostly waits, are paid by fewer CTAs), and the search with eight for
-// the rows that are left, so that one flat row does not hold up the batch.
+// costs, mostly waits, are paid by fewer CTAs), and the search with more of
+// them (eight, fewer where many rows may be left) for the rows that are left,
+// so that one flat row does not hold up the batch.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -1331,8 +1332,11 @@ __device__ inline int claim_row(const SampleArgs& a, SaShared& s, int start, int
 }
 
 // 128 registers a thread where the search runs: with 64 (two CTAs on an SM) it
-// spilled, and one row took 17 us instead of 13 by list and 51 instead of 35 by
-// search.  One cluster a row; the search's clusters take rows that are left, each when
+// spilled more, and one row took 17 us instead of 13 by list and 51 instead of
+// 35 by search.  What spills now (bytes stored a thread, fp32 and bf16): 152 and
+// 116 in the search, 32 and 44 where one launch does both, and 218 and 192 in
+// the list's own launch, whose 64 registers are worth it for many rows
+// (launch_sample_rows).  One cluster a row; the search's clusters take rows that are left, each when
 // it is done with its last (the rows cost very different times).
 template <typename T, int MODE>
 __global__ void __launch_bounds__(SA_THREADS, MODE == SA_LIST_ONLY ? 2 : 1)
