@@ -787,8 +787,8 @@ def orpo_norm_head_pass(X, norm_w, eps, head: Head, labels, layout, lam, sft_sco
 
 @dataclass
 class Fp8Head:
-    """A dense head in 8 bits for decoding: codes [V, D] and one scale for each
-    128 x 128 block."""
+    """A dense head in 8 bits for decoding (``cce_forward`` and the backward do
+    not take it): codes [V, D] and one scale for each 128 x 128 block."""
 
     q: torch.Tensor
     s: torch.Tensor

@@ -104,9 +104,10 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, uint32_t mask, uint
 // side is near the other's time and the hand-over between them is what is
 // left.  With real codes and scales 177 us in a long run, at 1.47 GHz under the
 // power cap.  2048 x 128256 x 4096: 1013 us cold, 1190 in a long run.  Measured
-// against this form when it took 1013: fma.rn.f32 instead of f32x2 1255 us, tiles of 256 x 128 with four accumulators 1343,
-// halves of 128 columns with accumulators of their own 1148, sixteen draining
-// warps 1614 (the instructions that are not FMAs add up).
+// against this form when it took 1013: fma.rn.f32 instead of f32x2 1255 us,
+// tiles of 256 x 128 with four accumulators 1343, halves of 128 columns with
+// accumulators of their own 1148, sixteen draining warps 1614 (the instructions
+// that are not FMAs add up).
 constexpr int F8_BM = 128, F8_BN = 256, F8_BK = 128;
 constexpr int F8_STAGES = 5;
 constexpr int F8_STAGE = (F8_BM + F8_BN / 2) * F8_BK;

@@ -198,8 +198,8 @@ cce_status launch_sample_rows(const SampleArgs& a, int64_t B, cudaStream_t st) {
     return launch_sample<T, SA_BOTH>(a, B, c, st);
   const cce_status s = launch_sample<T, SA_LIST_ONLY>(a, B, c, st);
   // Fewer CTAs a row where many rows may be left: 256 rows of 262,144 bf16
-  // logits, all of them flat, take 652 us with 2 and some 827 with 4; but 61 rows
-  // of 128,256, few of them flat, 73 us with 8 and some 102 with 2.
+  // logits, all of them flat, take 657 us with 2 and 827 with 4; but 61 rows of
+  // 128,256, few of them flat, 74 us with 8 and 102 with 2.
   int cs = most;
   while (cs > 1 && cs * B > 4 * sm_count_guess()) cs /= 2;
   return s != CCE_OK ? s : launch_sample<T, SA_SEARCH_ONLY>(a, B, cs, st);

@@ -681,7 +681,8 @@ class Sampler {
   // 2^104 / c below m, so those sums are nothing beside the new maximum.  In
   // fp64, since a rising row does this for each of a warp's segments (256 of
   // ex2.approx's errors of 2^-22 would be four times SA_SUM_ERROR).  Nothing
-  // too where the maxima are 2^-900 apart, which keeps a bounded unround() out.
+  // too where the maxima are a factor of 2^900 apart, so that unround()'s bound,
+// which is for sums of zero, never meets another.
   __device__ double rescale(float h, float next) const {
     const double x = double(h) - double(next);  // NaN, if both are infinite
     return x > -900.0 && fabsf(h) < INFINITY ? exp2_fp64(x) : 0.0;
@@ -1293,9 +1294,9 @@ __device__ void Sampler<T>::run() {
 // The next row, from `start` round the batch, that the list left undecided and
 // no cluster has claimed yet, now claimed; -1: none.  For a whole CTA.  A row
 // that was seen taken never comes back, so each CTA goes over the batch once,
-// 2,048 rows a step.  2^20 rows of 8 logits, none of them left: 16.0 ms in all;
-// 27.1 with one warp that went over 32 rows a step, again for each claim.  256
-// rows of 262,144, greedy: 49.2 us, 51.3.
+// 2,048 rows a step.  2^20 rows of 8 logits, none of them left: 16.0 ms in all,
+// 27.1 with one warp that went over 32 rows a step, again for each claim; 256
+// rows, none left: 2 us less.
 __device__ inline int claim_row(const SampleArgs& a, SaShared& s, int start, int& seen) {
   constexpr int EACH = 4, NONE = 0x7FFFFFFF;
   const int lane = threadIdx.x & 31;
@@ -1336,8 +1337,9 @@ __device__ inline int claim_row(const SampleArgs& a, SaShared& s, int start, int
 // 35 by search.  What spills now (bytes stored a thread, fp32 and bf16): 152 and
 // 116 in the search, 32 and 44 where one launch does both, and 218 and 192 in
 // the list's own launch, whose 64 registers are worth it for many rows
-// (launch_sample_rows).  One cluster a row; the search's clusters take rows that are left, each when
-// it is done with its last (the rows cost very different times).
+// (launch_sample_rows).  One cluster a row; the search's clusters take rows that
+// are left, each when it is done with its last (the rows cost very different
+// times).
 template <typename T, int MODE>
 __global__ void __launch_bounds__(SA_THREADS, MODE == SA_LIST_ONLY ? 2 : 1)
     sample_kernel(const __grid_constant__ SampleArgs a) {
